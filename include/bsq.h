@@ -23,6 +23,7 @@
  *      row FP8       [rows, K] E4M3 + FP32 [rows]
  *      block FP8     [N, K] E4M3 + FP32 [N/128, K/128]
  *      int8 per-32   [rows, K] int8 + FP32 [rows, K/32]
+ *      FP8 per-128   [rows, K] E4M3 + FP32 [rows, K/128]  (activations)
  *      outputs       BF16 [M, N]
  *  - The last argument is the CUDA stream (a cudaStream_t; NULL is the
  *    legacy default stream).  Every call is asynchronous and stream-ordered;
@@ -40,8 +41,8 @@
  *  - Concurrent calls on different streams may run concurrently; they share
  *    no device memory, except calls of int8_w4a8_prefill_noalloc, which share
  *    its scratch array and must not overlap on the GPU, and calls of
- *    int8_blockscaled_gemm_ws given the same workspace, which must not
- *    overlap either.
+ *    int8_blockscaled_gemm_ws, or of fp8_moe_blockscaled, given the same
+ *    workspace, which must not overlap either.
  *
  * Rounding: every quantised code and scale is defined bit-exactly (see each
  * function); GEMM and GEMV outputs are FP32 sums rounded once to BF16 and
@@ -378,6 +379,118 @@ BSQ_API bsq_status fp8_gemm_rowscale(const uint8_t *a, const float *a_scale,
                              const uint8_t *w, const float *w_scale,
                              uint16_t *out, int m, int n, int k,
                              bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * rmsnorm_residual_quant_fp8 -- root-mean-square norm with the residual's
+ * addition and an E4M3 output, in front of an FP8 projection.  No
+ * counterpart on the pages.
+ *   x            BF16 [m, k]
+ *   residual     BF16 [m, k] or NULL (nothing is added)
+ *   gain         BF16 [k]
+ *   eps          finite, >= 0
+ *   residual_out BF16 [m, k] or NULL: receives h.  It may be the same buffer
+ *                as x or as residual (no other overlap is allowed)
+ *   q            E4M3 [m, k] out
+ *   scale        FP32 out: group 128 -> [m, k/128], the activations of
+ *                fp8_gemm_blockscaled; group 0 -> [m], those of
+ *                fp8_gemm_rowscale
+ *   h = BF16_rne(x + residual) (FP32 sum; h = x without residual);
+ *   y = (h * r) * gain, r = 1 / sqrt(sum h^2 / k + eps), all in FP32 and not
+ *   rounded further; s = amax|y| / 448 over each group; q =
+ *   E4M3_rne_satfinite(y / s); an all-zero group gives s = 0 and q = 0.  A
+ *   row of zeros with eps = 0 gives zeros.
+ *   x, residual, gain, residual_out, q 16-byte aligned, scale 4-byte.
+ * Errors: k % 16 != 0, group not 0 or 128, group 128 with k % 128 != 0, eps
+ * negative or not finite -> INVALID_ARG; k > 65536 -> UNSUPPORTED.
+ * ---------------------------------------------------------------------- */
+BSQ_API bsq_status rmsnorm_residual_quant_fp8(const uint16_t *x, const uint16_t *residual,
+                                      const uint16_t *gain, float eps, uint16_t *residual_out,
+                                      uint8_t *q, float *scale, int group, int m, int k,
+                                      bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * quant_act_fp8_per128 -- BF16 [m, k] -> E4M3 [m, k] + FP32 [m, k/128], the
+ * activations of fp8_gemm_blockscaled (per token and 128 of K; the weight's
+ * 128 x 128 blocks are quant_blockfp8's).
+ *   Per group: s = amax / 448 (FP32); q = E4M3_rne_satfinite(x / s);
+ *   amax = 0 gives s = 0 and q = 0.
+ * Errors: k % 128 != 0 -> INVALID_ARG.  a, a_fp8 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+BSQ_API bsq_status quant_act_fp8_per128(const uint16_t *a, uint8_t *a_fp8, float *a_scale,
+                                int m, int k, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * silu_mul_quant_fp8_per128 -- the activation of a gated MLP, quantised for
+ * the down projection: gate_up BF16 [m, 2k] (the gate's k columns, then the
+ * up projection's k) -> E4M3 [m, k] + FP32 [m, k/128].
+ *   y = (g / (1 + exp(-g))) * u in FP32, not rounded further, then the codes
+ *   and scales of quant_act_fp8_per128 on y.  |y| must stay finite.
+ * Errors: k % 128 != 0 -> INVALID_ARG.  gate_up, a_fp8 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+BSQ_API bsq_status silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *a_fp8,
+                                     float *a_scale, int m, int k, bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_gemm_blockscaled -- the FP8 product of activations with one scale per
+ * token and 128 of K and a block FP8 weight, for any m (fp8_gemv_blockscaled
+ * takes BF16 activations, m <= 16).
+ *   a E4M3 [m, k] + a_scale FP32 [m, k/128]; w E4M3 [n, k] + w_scale FP32
+ *   [ceil(n/128), k/128] (n need not be a multiple of 128); out BF16 [m, n].
+ *   C[i,j] = sum_b a_scale[i,b] * w_scale[j/128,b] * sum_{k in b} a*w
+ * FP32 sums, one BF16 rounding.  a, w, out 16-byte aligned, scales 4-byte.
+ * Errors: k % 16 != 0 -> INVALID_ARG; k % 128 != 0 -> UNSUPPORTED.
+ * ---------------------------------------------------------------------- */
+BSQ_API bsq_status fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w,
+                                const float *w_scale, uint16_t *out, int m, int n, int k,
+                                bsq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_blockscaled -- a whole mixture-of-experts feed-forward for a few
+ * tokens (0 <= tokens <= 16, as the GEMVs): the choice of experts, the gate
+ * and up products, SiLU, the down product and the weighted sum.  Weights in
+ * the block FP8 format, activations BF16, as fp8_gemv_blockscaled.
+ *   x             BF16 [tokens, hidden]
+ *   logits        FP32 [tokens, experts], the router's scores
+ *   w_gate_up     E4M3 [experts, 2*inter, hidden]: an expert's inter gate
+ *                 rows, then its inter up rows
+ *   gate_up_scale FP32 [experts, 2*inter/128, hidden/128]
+ *   w_down        E4M3 [experts, hidden, inter]
+ *   down_scale    FP32 [experts, hidden/128, inter/128]
+ *   out           BF16 [tokens, hidden]
+ *   topk_ids      int32 [tokens, topk] out, or NULL
+ *   topk_weights  FP32 [tokens, topk] out, or NULL
+ *   workspace     device memory of fp8_moe_workspace_bytes(tokens, hidden,
+ *                 inter, topk) bytes, 16-byte aligned; needs no clearing.
+ *                 Calls that share a workspace must not overlap on the GPU
+ *                 (stream-ordered calls, and graphs replayed one after the
+ *                 other, may share).
+ * A token's experts are those of its topk largest logits, in falling order,
+ * the lowest index first among equals (-0 equals +0); NaN counts as -inf.
+ * With p_e = exp(l_e - max l) (0 for -inf), the weight of a chosen expert is
+ * p_e divided by the sum of p over the chosen experts (renormalise = 1) or
+ * over all (0); a token whose logits are all -inf gets weights 0 and an
+ * output of zeros.  An expert whose weight is 0 is not read for that token.
+ *   act = (g / (1 + exp(-g))) * u, g and u the gate and up products;
+ *   out[t] = sum_j weight[t,j] * (w_down[id_j] act_j)
+ * FP32 sums, one BF16 rounding; act is kept with 11 significant bits or
+ * more.  An output does not change from run to run.
+ * Errors: tokens outside 0..16, experts <= 0, topk outside 1..experts,
+ * hidden or inter not a positive multiple of 16, renormalise not 0 or 1,
+ * ws_bytes too small -> INVALID_ARG; hidden or inter not a multiple of 128,
+ * topk > 16, experts > 512, experts * 2*inter or experts * hidden above
+ * 2^31 - 1 -> UNSUPPORTED.  x, weights, out, workspace 16-byte aligned, the
+ * rest 4-byte.
+ * ---------------------------------------------------------------------- */
+BSQ_API bsq_status fp8_moe_blockscaled(const uint16_t *x, const float *logits, const uint8_t *w_gate_up,
+                               const float *gate_up_scale, const uint8_t *w_down,
+                               const float *down_scale, uint16_t *out, int32_t *topk_ids,
+                               float *topk_weights, void *workspace, size_t ws_bytes, int tokens,
+                               int hidden, int inter, int experts, int topk, int renormalise,
+                               bsq_stream_t stream);
+
+/* Workspace bytes of fp8_moe_blockscaled; 0 for a shape it refuses or when
+ * the device cannot be queried. */
+BSQ_API size_t fp8_moe_workspace_bytes(int tokens, int hidden, int inter, int topk);
 
 /* ------------------------------------------------------------------------
  * bsq_amax_bf16 -- max |x| over `count` BF16 values, written as one FP32 to

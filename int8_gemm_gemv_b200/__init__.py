@@ -21,6 +21,8 @@ __all__ = [
     "quant_rowwise_fp8",
     "quant_blockfp8", "requant_w_nvfp4_int8", "quant_act_int8_per32", "int8_blockscaled_gemm",
     "int8_w4a8_prefill", "int8_w4a8_prefill_noalloc", "requant_blockfp8_to_rowwise", "fp8_gemm_rowscale", "bsq_amax_bf16",
+    "rmsnorm_residual_quant_fp8", "quant_act_fp8_per128", "silu_mul_quant_fp8_per128", "fp8_gemm_blockscaled",
+    "fp8_moe_blockscaled", "fp8_moe_workspace_bytes",
     "status_string", "debug_launch_count", "debug_take_timeouts", "library_path", "lib",
 ]
 
@@ -63,6 +65,11 @@ _SIGS = {
     "int8_w4a8_prefill_noalloc": [_P, _P, _P, _P, _I, _I, _I, _P],
     "requant_blockfp8_to_rowwise": [_I, _P, _P, _I, _I, _P, _P, ctypes.POINTER(_P), ctypes.POINTER(_P), _P],
     "fp8_gemm_rowscale": [_P, _P, _P, _P, _P, _I, _I, _I, _P],
+    "rmsnorm_residual_quant_fp8": [_P, _P, _P, _F, _P, _P, _P, _I, _I, _I, _P],
+    "quant_act_fp8_per128": [_P, _P, _P, _I, _I, _P],
+    "silu_mul_quant_fp8_per128": [_P, _P, _P, _I, _I, _P],
+    "fp8_gemm_blockscaled": [_P, _P, _P, _P, _P, _I, _I, _I, _P],
+    "fp8_moe_blockscaled": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _I, _I, _I, _I, _I, _I, _P],
     "bsq_amax_bf16": [_P, ctypes.c_size_t, _P, _P],
     "bsq_debug_stream_read": [_P, ctypes.c_size_t, _P, _I, _P],
 }
@@ -93,6 +100,8 @@ def lib() -> ctypes.CDLL:
         L.bsq_debug_cuda_error_string.restype = ctypes.c_char_p
         L.int8_gemm_workspace_bytes.argtypes = []
         L.int8_gemm_workspace_bytes.restype = ctypes.c_size_t
+        L.fp8_moe_workspace_bytes.argtypes = [_I, _I, _I, _I]
+        L.fp8_moe_workspace_bytes.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -227,6 +236,40 @@ def requant_blockfp8_to_rowwise(tag, w, scale, n, k, w_out, scale_out, stream=No
 def fp8_gemm_rowscale(a, a_scale, w, w_scale, out, m, n, k, stream=None):
     _call("fp8_gemm_rowscale", _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(out), m, n, k,
           _stream(stream))
+
+
+def rmsnorm_residual_quant_fp8(x, residual, gain, eps, residual_out, q, scale, group, m, k, stream=None):
+    """residual and residual_out may be None; group 128 (scale [m, k/128]) or 0 (one scale per row)."""
+    _call("rmsnorm_residual_quant_fp8", _ptr(x), _ptr(residual), _ptr(gain), eps, _ptr(residual_out), _ptr(q),
+          _ptr(scale), group, m, k, _stream(stream))
+
+
+def quant_act_fp8_per128(a, a_fp8, a_scale, m, k, stream=None):
+    _call("quant_act_fp8_per128", _ptr(a), _ptr(a_fp8), _ptr(a_scale), m, k, _stream(stream))
+
+
+def silu_mul_quant_fp8_per128(gate_up, a_fp8, a_scale, m, k, stream=None):
+    """gate_up [m, 2k]: the gate's k columns, then the up projection's."""
+    _call("silu_mul_quant_fp8_per128", _ptr(gate_up), _ptr(a_fp8), _ptr(a_scale), m, k, _stream(stream))
+
+
+def fp8_gemm_blockscaled(a, a_scale, w, w_scale, out, m, n, k, stream=None):
+    _call("fp8_gemm_blockscaled", _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(out), m, n, k,
+          _stream(stream))
+
+
+def fp8_moe_workspace_bytes(tokens, hidden, inter, topk):
+    """Bytes of the workspace fp8_moe_blockscaled needs on the current device
+    (0 for a shape it refuses, or when the device cannot be queried)."""
+    return int(lib().fp8_moe_workspace_bytes(tokens, hidden, inter, topk))
+
+
+def fp8_moe_blockscaled(x, logits, w_gate_up, gate_up_scale, w_down, down_scale, out, topk_ids, topk_weights,
+                        workspace, ws_bytes, tokens, hidden, inter, experts, topk, renormalise, stream=None):
+    """topk_ids and topk_weights may be None; see include/bsq.h."""
+    _call("fp8_moe_blockscaled", _ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(gate_up_scale), _ptr(w_down),
+          _ptr(down_scale), _ptr(out), _ptr(topk_ids), _ptr(topk_weights), _ptr(workspace), ws_bytes, tokens, hidden,
+          inter, experts, topk, int(renormalise), _stream(stream))
 
 
 def bsq_amax_bf16(x, count, amax_dev, stream=None):

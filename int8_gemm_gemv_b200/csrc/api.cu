@@ -3,7 +3,9 @@
 // that fails it launches nothing and needs no GPU.
 #include <atomic>
 #include <cfloat>
+#include <climits>
 #include <cmath>
+#include <cstdint>
 
 #include "../../include/bsq.h"
 #include "bsq_internal.h"
@@ -244,6 +246,89 @@ bsq_status fp8_gemm_rowscale(const uint8_t *a, const float *a_scale, const uint8
     if (!a || !a_scale || !w || !w_scale || !out) return BSQ_ERR_INVALID_ARG;
     if (!al16(a) || !al16(w) || !al16(out) || !al4(a_scale) || !al4(w_scale)) return BSQ_ERR_MISALIGNED;
     return cuda_status(bsq::launch_fp8_gemm_rowscale(a, a_scale, w, w_scale, out, m, n, k, cs(stream)));
+}
+
+bsq_status rmsnorm_residual_quant_fp8(const uint16_t *x, const uint16_t *residual, const uint16_t *gain, float eps,
+                                      uint16_t *residual_out, uint8_t *q, float *scale, int group, int m, int k,
+                                      bsq_stream_t stream) {
+    if (m < 0 || k <= 0 || k % 16 || (group != 0 && group != 128) || (group == 128 && k % 128) ||
+        !std::isfinite(eps) || eps < 0.0f)
+        return BSQ_ERR_INVALID_ARG;
+    if (k > bsq::kRmsMaxK) return BSQ_ERR_UNSUPPORTED;
+    if (m == 0) return BSQ_OK;
+    if (!x || !gain || !q || !scale) return BSQ_ERR_INVALID_ARG;
+    if (!al16(x) || !al16(residual) || !al16(gain) || !al16(residual_out) || !al16(q) || !al4(scale))
+        return BSQ_ERR_MISALIGNED;
+    return cuda_status(
+        bsq::launch_rmsnorm_residual_quant_fp8(x, residual, gain, eps, residual_out, q, scale, group, m, k, cs(stream)));
+}
+
+bsq_status quant_act_fp8_per128(const uint16_t *a, uint8_t *a_fp8, float *a_scale, int m, int k, bsq_stream_t stream) {
+    if (m < 0 || k <= 0 || k % 128) return BSQ_ERR_INVALID_ARG;
+    if (m == 0) return BSQ_OK;
+    if (!a || !a_fp8 || !a_scale) return BSQ_ERR_INVALID_ARG;
+    if (!al16(a) || !al16(a_fp8) || !al4(a_scale)) return BSQ_ERR_MISALIGNED;
+    return cuda_status(bsq::launch_quant_act_fp8_per128(a, a_fp8, a_scale, m, k, cs(stream)));
+}
+
+bsq_status silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *a_fp8, float *a_scale, int m, int k,
+                                     bsq_stream_t stream) {
+    if (m < 0 || k <= 0 || k % 128) return BSQ_ERR_INVALID_ARG;
+    if (m == 0) return BSQ_OK;
+    if (!gate_up || !a_fp8 || !a_scale) return BSQ_ERR_INVALID_ARG;
+    if (!al16(gate_up) || !al16(a_fp8) || !al4(a_scale)) return BSQ_ERR_MISALIGNED;
+    return cuda_status(bsq::launch_silu_mul_quant_fp8_per128(gate_up, a_fp8, a_scale, m, k, cs(stream)));
+}
+
+bsq_status fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w, const float *w_scale,
+                                uint16_t *out, int m, int n, int k, bsq_stream_t stream) {
+    if (m < 0 || n < 0 || k <= 0 || k % 16) return BSQ_ERR_INVALID_ARG;
+    if (k % 128) return BSQ_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return BSQ_OK;
+    if (!a || !a_scale || !w || !w_scale || !out) return BSQ_ERR_INVALID_ARG;
+    if (!al16(a) || !al16(w) || !al16(out) || !al4(a_scale) || !al4(w_scale)) return BSQ_ERR_MISALIGNED;
+    return cuda_status(bsq::launch_fp8_gemm_blockscaled(a, a_scale, w, w_scale, out, m, n, k, cs(stream)));
+}
+
+namespace {
+
+bsq_status check_moe_shape(int tokens, int hidden, int inter, int topk) {
+    if (tokens < 0 || tokens > bsq::kMoeMaxTokens || hidden <= 0 || inter <= 0 || hidden % 16 || inter % 16 || topk < 1)
+        return BSQ_ERR_INVALID_ARG;
+    if (hidden % 128 || inter % 128 || topk > bsq::kMoeMaxTopk) return BSQ_ERR_UNSUPPORTED;
+    return BSQ_OK;
+}
+
+}  // namespace
+
+size_t fp8_moe_workspace_bytes(int tokens, int hidden, int inter, int topk) {
+    if (check_moe_shape(tokens, hidden, inter, topk) != BSQ_OK) return 0;
+    return bsq::fp8_moe_workspace_bytes(tokens, hidden, inter, topk);
+}
+
+bsq_status fp8_moe_blockscaled(const uint16_t *x, const float *logits, const uint8_t *w_gate_up,
+                               const float *gate_up_scale, const uint8_t *w_down, const float *down_scale,
+                               uint16_t *out, int32_t *topk_ids, float *topk_weights, void *workspace,
+                               size_t ws_bytes, int tokens, int hidden, int inter, int experts, int topk,
+                               int renormalise, bsq_stream_t stream) {
+    if (experts <= 0 || topk > experts || (renormalise != 0 && renormalise != 1)) return BSQ_ERR_INVALID_ARG;
+    bsq_status st = check_moe_shape(tokens, hidden, inter, topk);
+    if (st != BSQ_OK) return st;
+    // the copies address weight rows and K columns with 32-bit coordinates
+    if (experts > bsq::kMoeMaxExperts || (int64_t)experts * 2 * inter > INT32_MAX ||
+        (int64_t)experts * hidden > INT32_MAX)
+        return BSQ_ERR_UNSUPPORTED;
+    if (tokens == 0) return BSQ_OK;
+    if (!x || !logits || !w_gate_up || !gate_up_scale || !w_down || !down_scale || !out || !workspace)
+        return BSQ_ERR_INVALID_ARG;
+    if (!al16(x) || !al4(logits) || !al16(w_gate_up) || !al4(gate_up_scale) || !al16(w_down) || !al4(down_scale) ||
+        !al16(out) || !al4(topk_ids) || !al4(topk_weights) || !al16(workspace))
+        return BSQ_ERR_MISALIGNED;
+    const size_t need = bsq::fp8_moe_workspace_bytes(tokens, hidden, inter, topk);
+    if (ws_bytes < need) return BSQ_ERR_INVALID_ARG;
+    bsq::MoeArgs a = {x,   logits,   w_gate_up,    gate_up_scale, w_down, down_scale, out,     topk_ids,
+                      topk_weights, workspace, tokens, hidden, inter, experts, topk,   renormalise};
+    return cuda_status(bsq::launch_fp8_moe_blockscaled(a, cs(stream)));
 }
 
 bsq_status bsq_amax_bf16(const uint16_t *x, size_t count, float *amax_dev, bsq_stream_t stream) {

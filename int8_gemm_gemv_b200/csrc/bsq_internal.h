@@ -73,6 +73,38 @@ cudaError_t launch_quant_act_int8_per32(const uint16_t *a, int8_t *q, float *sca
                                         cudaStream_t s);
 cudaError_t launch_amax_bf16(const uint16_t *x, size_t count, float *amax, cudaStream_t s);
 
+// ---- launchers (act_fp8.cu) ----
+constexpr int kRmsMaxK = 65536;  // widest row of the fused norm
+// residual and residual_out may be NULL; group 0 (one scale per row) or 128
+cudaError_t launch_rmsnorm_residual_quant_fp8(const uint16_t *x, const uint16_t *residual, const uint16_t *gain,
+                                              float eps, uint16_t *residual_out, uint8_t *q, float *scale, int group,
+                                              int m, int k, cudaStream_t s);
+cudaError_t launch_quant_act_fp8_per128(const uint16_t *a, uint8_t *q, float *scale, int m, int k, cudaStream_t s);
+cudaError_t launch_silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *q, float *scale, int m, int k,
+                                             cudaStream_t s);
+
+// ---- launchers (gemm_fp8_block.cu) ----
+cudaError_t launch_fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w,
+                                        const float *w_scale, uint16_t *out, int m, int n, int k, cudaStream_t s);
+
+// ---- launchers (moe_fp8.cu) ----
+constexpr int kMoeMaxTokens = 16, kMoeMaxTopk = 16, kMoeMaxExperts = 512;
+struct MoeArgs {
+    const uint16_t *x;       // [tokens, hidden] BF16
+    const float *logits;     // [tokens, experts]
+    const uint8_t *w_gu;     // [experts, 2 * inter, hidden] E4M3, gate rows then up rows
+    const float *s_gu;       // [experts, 2 * inter / 128, hidden / 128]
+    const uint8_t *w_d;      // [experts, hidden, inter] E4M3
+    const float *s_d;        // [experts, hidden / 128, inter / 128]
+    uint16_t *out;           // [tokens, hidden] BF16
+    int32_t *topk_ids;       // [tokens, topk] or NULL
+    float *topk_weights;     // [tokens, topk] or NULL
+    void *workspace;
+    int tokens, hidden, inter, experts, topk, renormalise;
+};
+size_t fp8_moe_workspace_bytes(int tokens, int hidden, int inter, int topk);
+cudaError_t launch_fp8_moe_blockscaled(const MoeArgs &a, cudaStream_t s);
+
 // ---- launchers (stream_read.cu) ----
 // mode 0: one CTA per SM, 128 KB ring; mode 1: L2 prefetch of each CTA's
 // share before the stream dependency and a 64 KB ring (two CTAs per SM)

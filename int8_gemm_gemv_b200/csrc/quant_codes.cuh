@@ -205,6 +205,33 @@ __device__ __forceinline__ uint32_t e2m1x2_short(uint32_t w, uint64_t rr, uint64
     return f32x2_to_e2m1x2(q0, q1);
 }
 
+// Eight E4M3 codes of x / s (RNE, satfinite) packed little-endian; `br` is
+// bracket_of(s).
+__device__ __forceinline__ uint2 e4m3_codes_8(const float (&x)[8], float s, const Bracket &br) {
+    uint32_t w[4];
+    if (br.ok) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            float p0 = __fmul_rn(x[2 * j], br.lo), p1 = __fmul_rn(x[2 * j + 1], br.lo);
+            w[j] = f32x2_to_e4m3x2(p0, p1);
+            const uint32_t hi = f32x2_to_e4m3x2(__fmul_rn(x[2 * j], br.hi), __fmul_rn(x[2 * j + 1], br.hi));
+            if (w[j] != hi) {
+                pair_boundaries<5, 8>(x[2 * j], x[2 * j + 1], s, p0, p1, w[j], hi);
+                w[j] = f32x2_to_e4m3x2(p0, p1);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) w[j] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * j], s), __fdiv_rn(x[2 * j + 1], s));
+    }
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ void unpack_bf16_8(const uint4 &v, float (&x)[8]) {
+    x[0] = lo_bf16(v.x); x[1] = hi_bf16(v.x); x[2] = lo_bf16(v.y); x[3] = hi_bf16(v.y);
+    x[4] = lo_bf16(v.z); x[5] = hi_bf16(v.z); x[6] = lo_bf16(v.w); x[7] = hi_bf16(v.w);
+}
+
 // Eight x / d quotients (packed BF16 x) -> eight E2M1 nibbles in one 32-bit
 // word, element 0 in the lowest nibble.
 __device__ __forceinline__ uint32_t nvfp4_codes_8(const uint4 &v, float d, const Bracket &br) {
