@@ -51,6 +51,7 @@ uint32_t take_timeouts_quant();
 uint32_t take_timeouts_gemm_w4a4_small();
 uint32_t take_timeouts_gemm_fp8();
 uint32_t take_timeouts_gemm_int8();
+uint32_t take_timeouts_gemm_fp8_block();
 uint32_t take_timeouts_gemv();
 uint32_t take_timeouts_stream_read();
 
