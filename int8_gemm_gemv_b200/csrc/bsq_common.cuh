@@ -31,6 +31,21 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // never hang the GPU.  Legitimate waits last microseconds.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
+// One lane of a converged warp, chosen by elect.sync.  Inside a branch on it
+// the compiler knows that a single thread runs, and issues tensor-core and
+// copy instructions at their full rate; under `lane == 0` it does not (a
+// 128-wide MMA step then takes 146 cycles to issue instead of 90, and a commit
+// 85 more instead of none).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
 // ------------------------------------------------------------- mbarriers --
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
@@ -70,6 +85,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, unsign
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(timeout_flag, 1u);
+            return false;
+        }
+    }
+}
+
+// The same wait with the clock read only once in 256 polls: reading
+// %globaltimer takes longer than the waits of a finely pipelined kernel.
+__device__ __forceinline__ bool mbar_wait_poll(uint64_t *bar, uint32_t parity, unsigned int *timeout_flag) {
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 256; i++)
+            if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) {
             atomicOr(timeout_flag, 1u);
             return false;
         }

@@ -15,15 +15,23 @@
 // Per CTA (384 threads):
 //   warp 0      TMA producer, a six-stage ring of one K block each (16 KB of
 //               A, 16 KB of W), counted on the even CTA's barrier
-//   warp 1      tensor memory for the pair; in the even CTA, lane 0 issues
-//               four MMAs per block into one of two 256-column buffers, so
-//               the next block's products overlap this block's fold
+//   warp 1      tensor memory for the pair; in the even CTA, one thread
+//               issues the MMAs: per block and column half four of 256 x 128
+//               x 32 into one of that half's two 128-column buffers
+//   warp 2      brings the activation and weight scales into shared memory,
+//               four blocks at a time (one load per activation row and fold
+//               thread, straight from global memory, cost more than the MMAs)
 //   warps 4..11 fold and epilogue: warp w owns lane group w % 4 and column
 //               half (w - 4) / 4; output through swizzled shared memory and
 //               TMA stores (plain stores where a row is not a multiple of 16
 //               bytes)
 // Per SM and K block the MMAs take 512 cycles and the fold's 32,768 FMAs 256
-// of the FP32 lanes' cycles.
+// of the FP32 lanes' cycles.  A buffer goes round MMA (256 cycles), commit
+// (about 170), fold (about 450) and the arrival at the even CTA (about 150):
+// four buffers of 128 columns cover that, two of 256 columns (with 512 cycles
+// of MMA in the round) did not.  128 columns run at the tensor cores' full
+// rate as long as the issue takes less than 64 cycles per MMA, hence the
+// precomputed descriptors.
 //
 // Launched with programmatic stream serialization: every role waits for the
 // previous kernel (griddepcontrol.wait) before its first global access.
@@ -39,53 +47,49 @@ namespace {
 
 static __device__ unsigned int g_timeouts;
 
-template <int R> __device__ __forceinline__ void setmaxnreg_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R> __device__ __forceinline__ void setmaxnreg_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // (d0, d1) += (a0, a1) * (b0, b1), packed
 __device__ __forceinline__ void fma2(float2 &d, float2 a, float2 b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;"
         : "+l"(*reinterpret_cast<uint64_t *>(&d))
         : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
 }
 
 // Pair MMA: D (128 lanes of each CTA) (+)= A (128 rows in each CTA) x
-// B (N rows, half in each CTA), E4M3, issued by the even CTA.
-__device__ __forceinline__ void mma_f8f6f4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
+// B (N rows, half in each CTA), E4M3, issued by the even CTA.  The low words
+// of the descriptors (start address) vary; the high word is the same for all.
+__device__ __forceinline__ void mma_f8f6f4_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi,
+                                                uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
 namespace pair {
 
 constexpr int BM = 128;       // rows of A per CTA (256 per pair)
-constexpr int BN = 256;       // output columns per tile
-constexpr int BNH = BN / 2;   // weight rows per CTA
+constexpr int BN = 128;       // output columns per tile: one scale block
 constexpr int BK = 128;       // one scale block, in bytes = elements
-constexpr int STAGES = 6;
-constexpr int A_BYTES = BM * BK, B_BYTES = BNH * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int NBUF = 2, TMEM_COLS = 512;
+constexpr int STAGES = 7;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int NBUF = 4, TMEM_COLS = NBUF * BN;
 constexpr int kFoldWarps = 8, kThreads = 32 * (4 + kFoldWarps);
-// Launched with 168 registers a thread; warps 0-3 drop to 56, the two fold
-// warpgroups take 224: 128 * 56 + 256 * 224 = 384 * 168.  The launcher checks
-// the compiled count.
-constexpr int kLaunchRegs = 168, kCtlRegs = 56, kFoldRegs = 224;
-static_assert(128 * kCtlRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * kLaunchRegs, "register split");
 // output staging: per fold warp one TMA store box of 32 rows x 64 columns
 constexpr int OUT_BOX_COLS = 64, OUT_BOX_ROWS = 32, OUT_BOX_BYTES = OUT_BOX_COLS * 2 * OUT_BOX_ROWS;
 
+constexpr int SG = 4, SSLOTS = 3;  // scale blocks per slot, slots
+
 struct Smem {
+    float4 sa[SSLOTS][BM];  // this CTA's rows, SG consecutive blocks each
+    float4 sw[SSLOTS];
+    uint64_t sfull[SSLOTS], sempty[SSLOTS];
     uint64_t full[STAGES];   // even CTA: both CTAs' A and W tiles landed
     uint64_t empty[STAGES];  // both: the pair MMAs of this stage are done
     uint64_t tfull[NBUF];    // both: a block's products are in tensor memory
@@ -98,6 +102,21 @@ constexpr size_t kSmemBytes = 1024 + (size_t)STAGES * STAGE_BYTES + kFoldWarps *
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 __device__ __forceinline__ bool aborted(volatile Smem *s) { return s->abort != 0; }
+
+// Bounded wait that sets the abort flag when it runs out, and returns without
+// waiting once that flag is set.
+__device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, Smem *S) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (aborted(S)) return;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(&g_timeouts, 1u);
+            *(volatile uint32_t *)&S->abort = 1;
+            return;
+        }
+    }
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -123,9 +142,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S->full[s], 1);
             mbar_init(&S->empty[s], 1);
         }
-        for (int b = 0; b < NBUF; b++) {
-            mbar_init(&S->tfull[b], 1);
-            mbar_init(&S->tempty[b], 2 * kFoldWarps);
+        for (int i = 0; i < NBUF; i++) {
+            mbar_init(&S->tfull[i], 1);
+            mbar_init(&S->tempty[i], 2 * kFoldWarps);
+        }
+        for (int i = 0; i < SSLOTS; i++) {
+            mbar_init(&S->sfull[i], 1);
+            mbar_init(&S->sempty[i], kFoldWarps);
         }
         mbar_init(&S->drain, 1);
         S->abort = 0;
@@ -141,11 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = S->tmem_base;
     auto leader = [&](uint64_t *bar) { return mapa_shared(smem_u32(bar), 0); };
-    if (warp < 4) setmaxnreg_dec<kCtlRegs>();
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tensormap(&tmA);
             prefetch_tensormap(&tmB);
             dependency_wait();
@@ -153,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; t < num_tiles && ok; t += npairs) {
                 const int mt = t % tiles_m, nt = t / tiles_m;
-                const int arow = mt * 2 * BM + (int)rank * BM, brow = nt * BN + (int)rank * BNH;
+                const int arow = mt * 2 * BM + (int)rank * BM, brow = nt * BN + (int)rank * (BN / 2);
                 for (int kb = 0; kb < nkb; kb++, it++) {
                     const int s = it % STAGES;
                     if (!mbar_wait(&S->empty[s], ((it / STAGES) & 1) ^ 1, &g_timeouts) || aborted(S)) {
@@ -178,26 +200,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------ pair MMA issuer (even CTA)
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elect_one()) {
             const uint32_t idesc = idesc_e4m3(2 * BM, BN);
-            uint32_t it = 0;
+            const uint64_t desc0 = sdesc_k_sw128(smem_u32(a_tile(0)));
+            const uint32_t desc_hi = (uint32_t)(desc0 >> 32);
+            int s = 0;
+            uint32_t ph = 0, it = 0;
             bool ok = true;
             for (int t = pair; t < num_tiles && ok; t += npairs) {
-                for (int kb = 0; kb < nkb; kb++, it++) {
-                    const int s = it % STAGES, b = it % NBUF;
-                    if (!mbar_wait(&S->full[s], (it / STAGES) & 1, &g_timeouts) ||
-                        !mbar_wait_cluster(&S->tempty[b], ((it / NBUF) & 1) ^ 1, &g_timeouts) || aborted(S)) {
+                for (int kb = 0; kb < nkb && ok; kb++, it++) {
+                    if (!mbar_wait(&S->full[s], ph, &g_timeouts) || aborted(S)) {
+                        ok = false;
+                        break;
+                    }
+                    const int b = it % NBUF;
+                    if (!mbar_wait(&S->tempty[b], ((it / NBUF) & 1) ^ 1, &g_timeouts)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(a_tile(s)), b0 = smem_u32(b_tile(s));
+                    const uint32_t ad = (uint32_t)desc0 + s * (STAGE_BYTES >> 4), bd = ad + (A_BYTES >> 4);
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        mma_f8f6f4_pair(tmem + b * BN, sdesc_k_sw128(a0 + 32 * j), sdesc_k_sw128(b0 + 32 * j), idesc,
-                                        j != 0);
-                    tc_commit_pair_multicast(&S->empty[s], 0x3);
+                    for (int j = 0; j < 4; j++)  // 32 bytes of K each: 2 in the descriptor's address field
+                        mma_f8f6f4_pair(tmem + b * BN, ad + 2 * j, bd + 2 * j, desc_hi, idesc, j != 0);
                     tc_commit_pair_multicast(&S->tfull[b], 0x3);
+                    tc_commit_pair_multicast(&S->empty[s], 0x3);
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
             }
             if (!ok) S->abort = 1;
@@ -205,93 +236,122 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit_pair_multicast(&S->drain, 0x1);
             mbar_wait(&S->drain, 0, &g_timeouts);
         }
-    } else if (warp >= 4) {
-        // ------------------------------------------------- fold + epilogue
-        setmaxnreg_inc<kFoldRegs>();
-        const int q = warp & 3, h = (warp - 4) >> 2;
-        uint8_t *stage = out_stage + (warp - 4) * OUT_BOX_BYTES;
-        const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + h * 128;
-        if (lane == 0) prefetch_tensormap(&tmOut);
+    } else if (warp == 2) {
+        // ------------------------------------------------------- scales
         dependency_wait();
-        uint32_t it = 0;
+        const bool vec = (nkb & 3) == 0 &&
+                         ((reinterpret_cast<uintptr_t>(a_scale) | reinterpret_cast<uintptr_t>(w_scale)) & 15) == 0;
+        uint32_t g = 0;
         bool ok = true;
         for (int t = pair; t < num_tiles && ok; t += npairs) {
             const int mt = t % tiles_m, nt = t / tiles_m;
-            const int row0 = mt * 2 * BM + (int)rank * BM + 32 * q;  // first row of this warp
-            const int col0 = nt * BN + h * 128;
-            // rows and columns past the end read a valid scale; their products are zero or never stored
-            const float *sa = a_scale + (int64_t)min(row0 + lane, M - 1) * nkb;
-            const float *sw = w_scale + (int64_t)(min(col0, N - 1) >> 7) * nkb;
-            float2 acc[64];
+            // rows and columns past the end take a valid scale; their products are zero or never stored
+            const float *sa[4];
 #pragma unroll
-            for (int i = 0; i < 64; i++) acc[i] = make_float2(0.0f, 0.0f);
-            float sa_n = __ldg(sa), sw_n = __ldg(sw);
-            for (int kb = 0; kb < nkb; kb++, it++) {
-                const int b = it % NBUF;
-                const float f = sa_n * sw_n;
-                const float2 ff = make_float2(f, f);
-                if (kb + 1 < nkb) {
-                    sa_n = __ldg(sa + kb + 1);
-                    sw_n = __ldg(sw + kb + 1);
-                }
-                // (no abort-flag read here: if another role gives up, nothing more is committed and this
-                // bounded wait ends the fold)
-                ok = mbar_wait(&S->tfull[b], (it / NBUF) & 1, &g_timeouts);
+            for (int i = 0; i < 4; i++)
+                sa[i] = a_scale + (int64_t)min(mt * 2 * BM + (int)rank * BM + 32 * i + lane, M - 1) * nkb;
+            const float *sw = w_scale + (int64_t)nt * nkb;
+            for (int kb = 0; kb < nkb; kb += SG, g++) {
+                // loads first: they are in flight while the slot is waited for
+                auto four = [&](const float *p) {
+                    if (vec) return __ldg(reinterpret_cast<const float4 *>(p + kb));
+                    return make_float4(__ldg(p + kb), __ldg(p + min(kb + 1, nkb - 1)), __ldg(p + min(kb + 2, nkb - 1)),
+                                       __ldg(p + min(kb + 3, nkb - 1)));
+                };
+                float4 v[4], vw;
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[i] = four(sa[i]);
+                if (lane == 0) vw = four(sw);
+                const int s = g % SSLOTS;
+                ok = mbar_wait(&S->sempty[s], ((g / SSLOTS) & 1) ^ 1, &g_timeouts) && !aborted(S);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t src = tbase + b * BN;
-                uint32_t r0[32], r1[32];
-                auto fold = [&](const uint32_t(&r)[32], int c) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) S->sa[s][32 * i + lane] = v[i];
+                if (lane == 0) S->sw[s] = vw;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S->sfull[s]);
+            }
+        }
+        if (!ok && lane == 0) S->abort = 1;
+    } else if (warp >= 4) {
+        // ------------------------------------------------- fold + epilogue
+        // lane group q, column half h
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        uint8_t *stage = out_stage + (warp - 4) * OUT_BOX_BYTES;
+        const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + h * 64;
+        const uint32_t tempty0 = leader(&S->tempty[0]);
+        // arrivals through the cluster address even where the barrier is this
+        // CTA's: the plain form takes 160 cycles here, this one none
+        const uint32_t sempty0 = mapa_shared(smem_u32(&S->sempty[0]), rank);
+        if (lane == 0) prefetch_tensormap(&tmOut);
+        uint32_t it = 0, sph = 0;
+        int ss = 0;
+        for (int t = pair; t < num_tiles; t += npairs) {
+            const int mt = t % tiles_m, nt = t / tiles_m;
+            const int row0 = mt * 2 * BM + (int)rank * BM + 32 * q;  // first row of this warp
+            const int col0 = nt * BN + h * 64;
+            float2 acc[32];
+#pragma unroll
+            for (int i = 0; i < 32; i++) acc[i] = make_float2(0.0f, 0.0f);
+            for (int kb0 = 0; kb0 < nkb; kb0 += SG) {
+                wait_or_abort(&S->sfull[ss], sph, S);
+                const float4 xa = S->sa[ss][32 * q + lane], xw = S->sw[ss];
+                const float f[SG] = {xa.x * xw.x, xa.y * xw.y, xa.z * xw.z, xa.w * xw.w};
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(sempty0 + 8 * ss);
+                if (++ss == SSLOTS) {
+                    ss = 0;
+                    sph ^= 1;
+                }
+#pragma unroll
+                for (int j = 0; j < SG; j++) {
+                    if (kb0 + j >= nkb) break;
+                    // A wait that runs out sets the abort flag and goes on:
+                    // every later wait then returns at once, and all warps
+                    // reach the end without a vote in the loop.
+                    wait_or_abort(&S->tfull[it % NBUF], (it / NBUF) & 1, S);
+                    tc_fence_after();
+                    const float2 ff = make_float2(f[j], f[j]);
+                    uint32_t r0[32], r1[32];
+                    tmem_ld_32x32b_x32(tbase + (it % NBUF) * BN, r0);
+                    tmem_ld_32x32b_x32(tbase + (it % NBUF) * BN + 32, r1);
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * (it % NBUF));
 #pragma unroll
                     for (int i = 0; i < 16; i++)
-                        fma2(acc[16 * c + i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), ff);
-                };
-                tmem_ld_32x32b_x32(src, r0);
-                tmem_ld_wait();
-                tmem_ld_32x32b_x32(src + 32, r1);
-                fold(r0, 0);
-                tmem_ld_wait();
-                tmem_ld_32x32b_x32(src + 64, r0);
-                fold(r1, 1);
-                tmem_ld_wait();
-                tmem_ld_32x32b_x32(src + 96, r1);
-                fold(r0, 2);
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(leader(&S->tempty[b]));
-                fold(r1, 3);
+                        fma2(acc[i], make_float2(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1])), ff);
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        fma2(acc[16 + i], make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), ff);
+                    it++;
+                }
             }
-            if (!ok) {
-                if (lane == 0) S->abort = 1;
-                break;
-            }
+            // every lane leaves together
+            if (__any_sync(0xFFFFFFFFu, aborted(S))) break;
             if (use_tma_store) {
-                // box bx holds columns [64 bx, 64 bx + 64) of the warp's 32 x 128
-                // block; lane = row; 16-byte unit u of a row sits at u ^ (row & 7)
+                // the warp's 32 x 64 block; lane = row; 16-byte unit u of a row sits at u ^ (row & 7)
+                if (lane == 0) bulk_wait_group_read0();  // the previous store has read the box
+                __syncwarp();
 #pragma unroll
-                for (int bx = 0; bx < 2; bx++) {
-                    if (lane == 0) bulk_wait_group_read0();  // the previous store has read the box
-                    __syncwarp();
-#pragma unroll
-                    for (int u = 0; u < 8; u++) {
-                        const float2 *v = acc + 32 * bx + 4 * u;
-                        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                            make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                                       pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && row0 < M && col0 + bx * OUT_BOX_COLS < N) {
-                        tma_store_2d(&tmOut, stage, col0 + bx * OUT_BOX_COLS, row0);
-                        bulk_commit_group();
-                    }
+                for (int u = 0; u < 8; u++) {
+                    const float2 *v = acc + 4 * u;
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                   pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && row0 < M && col0 < N) {
+                    tma_store_2d(&tmOut, stage, col0, row0);
+                    bulk_commit_group();
                 }
             } else if (row0 + lane < M) {
                 uint16_t *orow = out + (int64_t)(row0 + lane) * N;
 #pragma unroll
-                for (int i = 0; i < 64; i++) {
+                for (int i = 0; i < 32; i++) {
                     const int n = col0 + 2 * i;
                     if (n < N) orow[n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i].x));
                     if (n + 1 < N) orow[n + 1] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i].y));
@@ -336,15 +396,10 @@ cudaError_t launch(const uint8_t *a, const float *a_scale, const uint8_t *w, con
     memset(&tO, 0, sizeof(tO));
     if (use_tma_store && !make_tmap_2d(&tO, out, 2, n, m, (uint64_t)n * 2, OUT_BOX_COLS, OUT_BOX_ROWS, true, false))
         return cudaErrorInvalidValue;
-    if (!make_tmap_2d(&tA, a, 1, k, m, k, BK, BM, true, false) || !make_tmap_2d(&tB, w, 1, k, n, k, BK, BNH, true, false))
+    if (!make_tmap_2d(&tA, a, 1, k, m, k, BK, BM, true, false) || !make_tmap_2d(&tB, w, 1, k, n, k, BK, BN / 2, true, false))
         return cudaErrorInvalidValue;
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        cudaFuncAttributes fa;
-        cudaError_t err = cudaFuncGetAttributes(&fa, k_gemm);
-        if (err != cudaSuccess) return err;
-        // a register split above the launch's total would wait forever
-        if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(k_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     });
     if (e != cudaSuccess) return e;
