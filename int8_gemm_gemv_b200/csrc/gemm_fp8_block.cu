@@ -77,12 +77,15 @@ namespace pair {
 constexpr int BM = 128;       // rows of A per CTA (256 per pair)
 constexpr int BN = 128;       // output columns per tile: one scale block
 constexpr int BK = 128;       // one scale block, in bytes = elements
-constexpr int STAGES = 7;
-constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int NBUF = 4, TMEM_COLS = NBUF * BN;
+constexpr int GB = 2;         // K blocks of one stage, one round of the barriers
+constexpr int STAGES = 4;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN / 2 * BK;  // of one K block
+constexpr int STAGE_BYTES = GB * (A_BYTES + B_BYTES);
+constexpr int NBUF = 2, TMEM_COLS = NBUF * GB * BN;
 constexpr int kFoldWarps = 8, kThreads = 32 * (4 + kFoldWarps);
-// output staging: per fold warp one TMA store box of 32 rows x 64 columns
-constexpr int OUT_BOX_COLS = 64, OUT_BOX_ROWS = 32, OUT_BOX_BYTES = OUT_BOX_COLS * 2 * OUT_BOX_ROWS;
+// output staging: per fold warp one TMA store box of 32 rows x 32 columns
+// (64-byte rows, 64-byte swizzle), used twice per tile
+constexpr int OUT_BOX_COLS = 32, OUT_BOX_ROWS = 32, OUT_BOX_BYTES = OUT_BOX_COLS * 2 * OUT_BOX_ROWS;
 
 constexpr int SG = 4, SSLOTS = 3;  // scale blocks per slot, slots
 
@@ -127,14 +130,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *out_stage = base + (size_t)STAGES * STAGE_BYTES;
     Smem *S = reinterpret_cast<Smem *>(out_stage + kFoldWarps * OUT_BOX_BYTES);
     auto a_tile = [&](int s) { return base + (size_t)s * STAGE_BYTES; };
-    auto b_tile = [&](int s) { return base + (size_t)s * STAGE_BYTES + A_BYTES; };
+    auto b_tile = [&](int s) { return base + (size_t)s * STAGE_BYTES + GB * A_BYTES; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int tiles_m = (M + 2 * BM - 1) / (2 * BM), tiles_n = (N + BN - 1) / BN;
     const int num_tiles = tiles_m * tiles_n;
-    const int nkb = K / BK;
+    const int nkb = K / BK, ngr = (nkb + GB - 1) / GB;
 
     launch_dependents();
     if (threadIdx.x == 0) {
@@ -170,22 +173,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             prefetch_tensormap(&tmA);
             prefetch_tensormap(&tmB);
+            const uint32_t full0 = leader(&S->full[0]);
             dependency_wait();
-            uint32_t it = 0;
-            bool ok = true;
+            uint32_t it = 0, ph = 1;
+            int s = 0;
+            bool ok = true, ready = mbar_test(&S->empty[0], 1);
             for (int t = pair; t < num_tiles && ok; t += npairs) {
                 const int mt = t % tiles_m, nt = t / tiles_m;
                 const int arow = mt * 2 * BM + (int)rank * BM, brow = nt * BN + (int)rank * (BN / 2);
-                for (int kb = 0; kb < nkb; kb++, it++) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait(&S->empty[s], ((it / STAGES) & 1) ^ 1, &g_timeouts) || aborted(S)) {
+                for (int g = 0; g < ngr; g++, it++) {
+                    if (!ready && (!mbar_wait(&S->empty[s], ph, &g_timeouts) || aborted(S))) {
                         ok = false;
                         break;
                     }
+                    // the next slot's barrier, read while this slot's copies are issued
+                    const int s1 = s + 1 == STAGES ? 0 : s + 1;
+                    const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
+                    ready = mbar_test(&S->empty[s1], ph1);
                     if (rank == 0) mbar_arrive_expect_tx(&S->full[s], 2 * STAGE_BYTES);
-                    const uint32_t bar = leader(&S->full[s]);
-                    tma_load_2d_pair(a_tile(s), &tmA, bar, kb * BK, arow);
-                    tma_load_2d_pair(b_tile(s), &tmB, bar, kb * BK, brow);
+                    const uint32_t bar = full0 + 8 * s;
+                    // [block][row][128 B]; a block past K is filled with zeros
+                    tma_load_3d_pair(a_tile(s), &tmA, bar, 0, arow, g * GB);
+                    tma_load_3d_pair(b_tile(s), &tmB, bar, 0, brow, g * GB);
+                    s = s1;
+                    ph = ph1;
                 }
             }
             if (!ok) {
@@ -204,31 +215,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc = idesc_e4m3(2 * BM, BN);
             const uint64_t desc0 = sdesc_k_sw128(smem_u32(a_tile(0)));
             const uint32_t desc_hi = (uint32_t)(desc0 >> 32);
-            int s = 0;
-            uint32_t ph = 0, it = 0;
-            bool ok = true;
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;
+            bool ok = true, ready = false;
             for (int t = pair; t < num_tiles && ok; t += npairs) {
-                for (int kb = 0; kb < nkb && ok; kb++, it++) {
-                    if (!mbar_wait(&S->full[s], ph, &g_timeouts) || aborted(S)) {
-                        ok = false;
-                        break;
-                    }
-                    const int b = it % NBUF;
-                    if (!mbar_wait(&S->tempty[b], ((it / NBUF) & 1) ^ 1, &g_timeouts)) {
+                for (int g = 0; g < ngr; g++) {
+                    if (!ready && (!mbar_wait(&S->full[s], ph, &g_timeouts) ||
+                                   !mbar_wait(&S->tempty[b], bph, &g_timeouts) || aborted(S))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t ad = (uint32_t)desc0 + s * (STAGE_BYTES >> 4), bd = ad + (A_BYTES >> 4);
+                    // the next stage's barriers, read while this one's MMAs
+                    // are issued
+                    const int s1 = s + 1 == STAGES ? 0 : s + 1, b1 = (b + 1) % NBUF;
+                    const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph, bph1 = b1 == 0 ? bph ^ 1 : bph;
+                    const bool r0 = mbar_test(&S->full[s1], ph1), r1 = mbar_test(&S->tempty[b1], bph1);
+                    const uint32_t ad = (uint32_t)desc0 + s * (STAGE_BYTES >> 4), bd = ad + (GB * A_BYTES >> 4);
 #pragma unroll
-                    for (int j = 0; j < 4; j++)  // 32 bytes of K each: 2 in the descriptor's address field
-                        mma_f8f6f4_pair(tmem + b * BN, ad + 2 * j, bd + 2 * j, desc_hi, idesc, j != 0);
+                    for (int u = 0; u < GB; u++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++)  // 32 bytes of K each: 2 in the descriptor's address field
+                            mma_f8f6f4_pair(tmem + (b * GB + u) * BN, ad + u * (A_BYTES >> 4) + 2 * j,
+                                            bd + u * (B_BYTES >> 4) + 2 * j, desc_hi, idesc, j != 0);
                     tc_commit_pair_multicast(&S->tfull[b], 0x3);
                     tc_commit_pair_multicast(&S->empty[s], 0x3);
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                    ready = r0 && r1;
+                    s = s1, b = b1;
+                    ph = ph1, bph = bph1;
                 }
             }
             if (!ok) S->abort = 1;
@@ -253,10 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *sw = w_scale + (int64_t)nt * nkb;
             for (int kb = 0; kb < nkb; kb += SG, g++) {
                 // loads first: they are in flight while the slot is waited for
-                auto four = [&](const float *p) {
+                auto four = [&](const float *p) {  // zeros past the last block
                     if (vec) return __ldg(reinterpret_cast<const float4 *>(p + kb));
-                    return make_float4(__ldg(p + kb), __ldg(p + min(kb + 1, nkb - 1)), __ldg(p + min(kb + 2, nkb - 1)),
-                                       __ldg(p + min(kb + 3, nkb - 1)));
+                    return make_float4(__ldg(p + kb), kb + 1 < nkb ? __ldg(p + kb + 1) : 0.0f,
+                                       kb + 2 < nkb ? __ldg(p + kb + 2) : 0.0f, kb + 3 < nkb ? __ldg(p + kb + 3) : 0.0f);
                 };
                 float4 v[4], vw;
 #pragma unroll
@@ -285,8 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // CTA's: the plain form takes 160 cycles here, this one none
         const uint32_t sempty0 = mapa_shared(smem_u32(&S->sempty[0]), rank);
         if (lane == 0) prefetch_tensormap(&tmOut);
-        uint32_t it = 0, sph = 0;
-        int ss = 0;
+        uint32_t bph = 0, sph = 0;
+        int b = 0, ss = 0;
+        bool ready = false;
         for (int t = pair; t < num_tiles; t += npairs) {
             const int mt = t % tiles_m, nt = t / tiles_m;
             const int row0 = mt * 2 * BM + (int)rank * BM + 32 * q;  // first row of this warp
@@ -297,56 +312,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kb0 = 0; kb0 < nkb; kb0 += SG) {
                 wait_or_abort(&S->sfull[ss], sph, S);
                 const float4 xa = S->sa[ss][32 * q + lane], xw = S->sw[ss];
-                const float f[SG] = {xa.x * xw.x, xa.y * xw.y, xa.z * xw.z, xa.w * xw.w};
+                float f0 = xa.x * xw.x, f1 = xa.y * xw.y;
+                const float f2 = xa.z * xw.z, f3 = xa.w * xw.w;
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(sempty0 + 8 * ss);
                 if (++ss == SSLOTS) {
                     ss = 0;
                     sph ^= 1;
                 }
-#pragma unroll
-                for (int j = 0; j < SG; j++) {
-                    if (kb0 + j >= nkb) break;
+#pragma unroll 1
+                for (int j = 0; j < min(SG, nkb - kb0); j += GB) {
                     // A wait that runs out sets the abort flag and goes on:
                     // every later wait then returns at once, and all warps
                     // reach the end without a vote in the loop.
-                    wait_or_abort(&S->tfull[it % NBUF], (it / NBUF) & 1, S);
+                    if (!ready) wait_or_abort(&S->tfull[b], bph, S);
+                    __syncwarp();
                     tc_fence_after();
-                    const float2 ff = make_float2(f[j], f[j]);
-                    uint32_t r0[32], r1[32];
-                    tmem_ld_32x32b_x32(tbase + (it % NBUF) * BN, r0);
-                    tmem_ld_32x32b_x32(tbase + (it % NBUF) * BN + 32, r1);
+                    const uint32_t src = tbase + b * GB * BN;
+                    uint32_t r[64];
+                    auto fold = [&](float f1) {
+                        const float2 ff = make_float2(f1, f1);
+#pragma unroll
+                        for (int i = 0; i < 32; i++)
+                            fma2(acc[i], make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), ff);
+                    };
+                    tmem_ld_32x32b_x64(src, r);
+                    tmem_ld_wait();
+                    fold(f0);
+                    tmem_ld_32x32b_x64(src + BN, r);
                     tmem_ld_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * (it % NBUF));
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        fma2(acc[i], make_float2(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1])), ff);
-#pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        fma2(acc[16 + i], make_float2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), ff);
-                    it++;
+                    if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * b);
+                    // the next stage's barrier, read while this one is folded
+                    b = (b + 1) % NBUF;
+                    bph ^= b == 0;
+                    ready = mbar_test(&S->tfull[b], bph);
+                    fold(f1);  // (past an odd last block: zeros times a scale of zero)
+                    f0 = f2, f1 = f3;
                 }
             }
             // every lane leaves together
             if (__any_sync(0xFFFFFFFFu, aborted(S))) break;
             if (use_tma_store) {
-                // the warp's 32 x 64 block; lane = row; 16-byte unit u of a row sits at u ^ (row & 7)
-                if (lane == 0) bulk_wait_group_read0();  // the previous store has read the box
-                __syncwarp();
+                // box bx holds columns [32 bx, 32 bx + 32) of the warp's 32 x 64
+                // block; lane = row; 16-byte unit u of a row sits at u ^ ((row >> 1) & 3)
 #pragma unroll
-                for (int u = 0; u < 8; u++) {
-                    const float2 *v = acc + 4 * u;
-                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                        make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                                   pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0 && row0 < M && col0 < N) {
-                    tma_store_2d(&tmOut, stage, col0, row0);
-                    bulk_commit_group();
+                for (int bx = 0; bx < 2; bx++) {
+                    if (lane == 0) bulk_wait_group_read0();  // the previous store has read the box
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        const float2 *v = acc + 16 * bx + 4 * u;
+                        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                       pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < M && col0 + bx * OUT_BOX_COLS < N) {
+                        tma_store_2d(&tmOut, stage, col0 + bx * OUT_BOX_COLS, row0);
+                        bulk_commit_group();
+                    }
                 }
             } else if (row0 + lane < M) {
                 uint16_t *orow = out + (int64_t)(row0 + lane) * N;
@@ -394,9 +421,12 @@ cudaError_t launch(const uint8_t *a, const float *a_scale, const uint8_t *w, con
     // TMA stores need 16-byte output rows
     const int use_tma_store = (n % 8) == 0;
     memset(&tO, 0, sizeof(tO));
-    if (use_tma_store && !make_tmap_2d(&tO, out, 2, n, m, (uint64_t)n * 2, OUT_BOX_COLS, OUT_BOX_ROWS, true, false))
-        return cudaErrorInvalidValue;
-    if (!make_tmap_2d(&tA, a, 1, k, m, k, BK, BM, true, false) || !make_tmap_2d(&tB, w, 1, k, n, k, BK, BN / 2, true, false))
+    if (use_tma_store) {
+        const uint64_t d[2] = {(uint64_t)n, (uint64_t)m}, st[1] = {(uint64_t)n * 2};
+        const uint32_t box[2] = {OUT_BOX_COLS, OUT_BOX_ROWS};
+        if (!make_tmap(&tO, out, 2, 2, d, st, box, 64)) return cudaErrorInvalidValue;
+    }
+    if (!make_tmap_rows_chunks(&tA, a, k, m, BM, GB) || !make_tmap_rows_chunks(&tB, w, k, n, BN / 2, GB))
         return cudaErrorInvalidValue;
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
