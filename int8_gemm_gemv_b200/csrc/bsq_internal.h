@@ -52,6 +52,7 @@ uint32_t take_timeouts_gemm_w4a4_small();
 uint32_t take_timeouts_gemm_fp8();
 uint32_t take_timeouts_gemm_int8();
 uint32_t take_timeouts_gemm_fp8_block();
+uint32_t take_timeouts_gemm_fp8_block_small();
 uint32_t take_timeouts_gemv();
 uint32_t take_timeouts_stream_read();
 
@@ -87,6 +88,12 @@ cudaError_t launch_silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *q
 // ---- launchers (gemm_fp8_block.cu) ----
 cudaError_t launch_fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w,
                                         const float *w_scale, uint16_t *out, int m, int n, int k, cudaStream_t s);
+
+// Few activation rows (gemm_fp8_block_small.cu): swapped operands, K split over
+// the CTAs of a cluster.
+cudaError_t launch_fp8_gemm_blockscaled_small(const uint8_t *a, const float *a_scale, const uint8_t *w,
+                                              const float *w_scale, uint16_t *out, int m, int n, int k,
+                                              cudaStream_t s);
 
 // ---- launchers (moe_fp8.cu) ----
 constexpr int kMoeMaxTokens = 16, kMoeMaxTopk = 16, kMoeMaxExperts = 512;

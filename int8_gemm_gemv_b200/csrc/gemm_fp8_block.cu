@@ -464,9 +464,17 @@ uint32_t take_timeouts_gemm_fp8_block() {
     return v;
 }
 
+// The swapped-operand kernel up to 64 rows (64 x 17408 x 5120: 19.4 us against
+// 23.9 here; 64 x 5120 x 5120: 11.6 against 13.3), and beyond while its tiles
+// of 128 x 32 outputs fit one to an SM (128 x 2112 x 5120, 68 tiles: 9.7 us
+// against 12.5; 256 x 2112 x 5120, 136 tiles: 12.7 both; 128 x 5120 x 5120,
+// 160 tiles: 17.5 against 13.6).
 cudaError_t launch_fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w,
                                         const float *w_scale, uint16_t *out, int m, int n, int k, cudaStream_t s) {
-    const cudaError_t e = pair::launch(a, a_scale, w, w_scale, out, m, n, k, s);
+    const int64_t small_tiles = (int64_t)((n + 127) / 128) * ((m + 31) / 32);
+    const cudaError_t e = m <= 64 || small_tiles <= sm_count()
+                              ? launch_fp8_gemm_blockscaled_small(a, a_scale, w, w_scale, out, m, n, k, s)
+                              : pair::launch(a, a_scale, w, w_scale, out, m, n, k, s);
     if (e == cudaSuccess) note_launch();
     return e;
 }
