@@ -372,7 +372,7 @@ uint32_t bsq_debug_take_timeouts(void) {
     return bsq::take_timeouts_gemm_w4a4() | bsq::take_timeouts_gemm_w4a4_small() | bsq::take_timeouts_gemm_fp8() |
            bsq::take_timeouts_gemm_int8() | bsq::take_timeouts_gemv() | bsq::take_timeouts_quant() |
            bsq::take_timeouts_stream_read() | bsq::take_timeouts_gemm_fp8_block() |
-           bsq::take_timeouts_gemm_fp8_block_small();
+           bsq::take_timeouts_gemm_fp8_block_small() | bsq::take_timeouts_moe();
 }
 
 }  // extern "C"

@@ -53,6 +53,7 @@ uint32_t take_timeouts_gemm_fp8();
 uint32_t take_timeouts_gemm_int8();
 uint32_t take_timeouts_gemm_fp8_block();
 uint32_t take_timeouts_gemm_fp8_block_small();
+uint32_t take_timeouts_moe();
 uint32_t take_timeouts_gemv();
 uint32_t take_timeouts_stream_read();
 

@@ -4,21 +4,84 @@
 //   act[t, j] = silu(Wg[e_j] x_t) * (Wu[e_j] x_t)
 //   out[t] = sum_j p[t, j] Wd[e_j] act[t, j]
 //
-// Plain form: one warp per token routes, one warp per intermediate element,
-// one warp per output element.
-#include <cfloat>
+// The reached experts' weights, read once, are the whole cost, so both kernels
+// are streaming reads built like the FP8 GEMV: one CTA per SM, a TMA producer
+// warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, and
+// sixteen consumer warps that split a box's K into 64-byte chunks (E4M3 ->
+// FP16 exactly, FP16 MMAs with FP32 sums, each chunk's sum times its block
+// scale).  The MMA's eight (or sixteen) columns are the tokens themselves: a
+// token that did not choose the expert has zeros there, which costs nothing
+// beside the stream, and no gather or scatter is needed.
+//
+//   k_moe_gate_up  every CTA routes all tokens by itself (some hundred
+//                  instructions per token), then takes an equal share of the
+//                  (expert, 16 intermediate rows) pairs: a box of gate rows
+//                  and one of up rows give silu(g) * u on the spot.  act is
+//                  kept as FP16 times a power of two per 16 values, 11
+//                  significant bits.
+//   k_moe_down     an output tile of 32 rows runs over all reached experts'
+//                  K, so a token's experts add up in registers.  The (tile,
+//                  expert, K) steps are cut into equal shares, one per CTA,
+//                  also inside a tile: 448 tiles on 148 SMs would otherwise
+//                  leave a quarter of them idle.  CTAs that share a tile leave
+//                  their FP32 sums in the workspace, and the last one to come
+//                  adds them in share order, so the result does not depend on
+//                  which was last.  No CTA waits for another.
+//
+// Both are launched with programmatic stream serialization.  The first lets
+// the second start as its own CTAs run out; that one reads the logits and the
+// weights, which the first does not write, and waits for it before act.
 #include <cmath>
 
-#include "bsq_common.cuh"
+#include "gemv_frag.cuh"
+
+#include <cuda_fp16.h>
 
 namespace bsq {
 
 namespace {
 
-struct Routing {
-    int32_t id[kMoeMaxTokens * kMoeMaxTopk];
-    float weight[kMoeMaxTokens * kMoeMaxTopk];
+using namespace gv;
+
+constexpr int kConsumers = 16;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kMaxSlots = 24;
+constexpr int kMaxActive = kMoeMaxTokens * kMoeMaxTopk;
+constexpr int kSums = 512;  // output sums of a group: tiles x (8 or 16 tokens) x 16 rows, at most
+
+static __device__ unsigned int g_timeouts;
+
+struct alignas(16) Route {
+    float weight[kMoeMaxTokens][kMoeMaxTopk];
+    uint16_t id[kMoeMaxTokens][kMoeMaxTopk];
+    uint32_t slot[kMoeMaxExperts];      // by expert: its tokens, then its place in `expert`
+    uint16_t expert[kMaxActive];        // the reached experts, in order
+    uint16_t tokens[kMaxActive];        // their tokens, a bit each
+    uint8_t pick[kMaxActive][kMoeMaxTokens];  // which of the token's choices the expert is
+    int warp_count[kConsumers];
+    int active;
 };
+
+struct alignas(16) Bars {
+    uint64_t full[kMaxSlots];
+    uint64_t empty[kMaxSlots];
+    uint32_t rowmax[kMoeMaxTokens];
+    uint32_t abort;
+    uint32_t last;  // this CTA finishes the tile
+};
+
+// Box geometry: `chunks` 64-byte chunks of K per box, `steps` boxes along K,
+// `slots` boxes in the ring.
+struct Ring {
+    int chunks, steps, slots;
+};
+
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+}
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------- routing --
 
 // Order-preserving key of a logit: NaN counts as -inf, -0 as +0.
 __device__ __forceinline__ uint32_t logit_key(float l) {
@@ -36,108 +99,688 @@ __device__ __forceinline__ float route_exp(float l, float mx) {
     return l == mx ? 1.0f : expf(l - mx);
 }
 
-__global__ void k_moe_route(MoeArgs a, Routing *R) {
-    const int t = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (t >= a.tokens) return;
+// Routes every token (one warp each) and lists the reached experts.  Called
+// by all threads of the CTA.
+__device__ __forceinline__ void route(const MoeArgs &a, Route *R) {
     constexpr int PER = kMoeMaxExperts / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t key[PER];
-    for (int i = 0; i < PER; i++) {
-        const int e = lane + 32 * i;
-        key[i] = e < a.experts ? logit_key(a.logits[t * a.experts + e]) : 0u;
-    }
-    uint32_t taken = 0;
-    float mx = 0.0f, sum = 0.0f, sum_all = 0.0f;
-    for (int j = 0; j < a.topk; j++) {
-        uint32_t best = 0;
-        for (int i = 0; i < PER; i++)
-            if (!((taken >> i) & 1)) best = max(best, key[i]);
-        best = __reduce_max_sync(0xFFFFFFFFu, best);
-        int e = 1 << 30;
-        for (int i = PER - 1; i >= 0; i--)
-            if (!((taken >> i) & 1) && key[i] == best && lane + 32 * i < a.experts) e = lane + 32 * i;
-        e = __reduce_min_sync(0xFFFFFFFFu, e);
-        if ((e & 31) == lane) taken |= 1u << (e >> 5);
-        const float l = key_logit(best);
-        if (j == 0) mx = l;
-        const float p = route_exp(l, mx);
-        sum += p;
-        if (lane == 0) {
-            R->id[t * a.topk + j] = e;
-            R->weight[t * a.topk + j] = p;
+    if (warp < a.tokens) {
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int e = lane + 32 * i;
+            key[i] = e < a.experts ? logit_key(__ldg(a.logits + (int64_t)warp * a.experts + e)) : 0u;
         }
     }
-    for (int i = 0; i < PER; i++)
-        if (lane + 32 * i < a.experts) sum_all += route_exp(key_logit(key[i]), mx);
-    for (int o = 16; o > 0; o >>= 1) sum_all += __shfl_xor_sync(0xFFFFFFFFu, sum_all, o);
-    if (!a.renormalise) sum = sum_all;
-    __syncwarp();
-    for (int j = lane; j < a.topk; j += 32) {
-        const float p = sum > 0.0f ? R->weight[t * a.topk + j] / sum : 0.0f;
-        R->weight[t * a.topk + j] = p;
-        if (a.topk_ids) a.topk_ids[t * a.topk + j] = R->id[t * a.topk + j];
-        if (a.topk_weights) a.topk_weights[t * a.topk + j] = p;
+    for (int e = threadIdx.x; e < kMoeMaxExperts; e += kThreads) R->slot[e] = 0;
+    __syncthreads();
+    if (warp < a.tokens) {
+        uint32_t taken = 0;
+        float mx = 0.0f, sum = 0.0f, mine = 0.0f;
+        int my_id = 0;
+        for (int j = 0; j < a.topk; j++) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < PER; i++)
+                if (32 * i < a.experts && !((taken >> i) & 1)) best = max(best, key[i]);
+            best = __reduce_max_sync(0xFFFFFFFFu, best);
+            int e = kMoeMaxExperts - 1;
+#pragma unroll
+            for (int i = PER - 1; i >= 0; i--)
+                if (32 * i < a.experts && !((taken >> i) & 1) && key[i] == best && lane + 32 * i < a.experts)
+                    e = lane + 32 * i;
+            e = __reduce_min_sync(0xFFFFFFFFu, e);
+            if ((e & 31) == lane) taken |= 1u << (e >> 5);
+            const float l = key_logit(best);
+            if (j == 0) mx = l;
+            const float p = route_exp(l, mx);
+            sum += p;
+            if (lane == j) {
+                mine = p;
+                my_id = e;
+            }
+        }
+        if (!a.renormalise) {
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; i++)
+                if (lane + 32 * i < a.experts) sum += route_exp(key_logit(key[i]), mx);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        }
+        if (lane < a.topk) {
+            const float w = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;
+            R->id[warp][lane] = (uint16_t)my_id;
+            R->weight[warp][lane] = w;
+            // an expert that adds nothing is not read
+            if (w > 0.0f) atomicOr(&R->slot[my_id], 1u << warp);
+        }
+    }
+    __syncthreads();
+    uint32_t mask = 0, ballot = 0;
+    if (warp < kConsumers) {
+        mask = R->slot[threadIdx.x];
+        ballot = __ballot_sync(0xFFFFFFFFu, mask != 0);
+        if (lane == 0) R->warp_count[warp] = __popc(ballot);
+    }
+    __syncthreads();
+    if (warp < kConsumers) {
+        int at = __popc(ballot & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; w++) at += R->warp_count[w];
+        if (mask) {
+            R->expert[at] = (uint16_t)threadIdx.x;
+            R->tokens[at] = (uint16_t)mask;
+            R->slot[threadIdx.x] = at;
+        }
+        if (threadIdx.x == 32 * kConsumers - 1) R->active = at + (mask != 0);
+    }
+    __syncthreads();
+    const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
+    if (t < a.tokens && j < a.topk && R->weight[t][j] > 0.0f) R->pick[R->slot[R->id[t][j]]][t] = (uint8_t)j;
+    __syncthreads();
+}
+static_assert(32 * kConsumers == kMoeMaxExperts && kMoeMaxTopk == 16, "one thread per expert, 16 choices");
+
+// ------------------------------------------------------------------- ring --
+
+// Consumer side of the ring: every consumer warp takes every box.
+struct Taker {
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    // The chunk of this warp in the next box (f.wa, f.wb), and the box given
+    // back.  After a timeout the warp keeps its loop and barrier sequence (so
+    // no other warp waits on it) but touches no slot.
+    template <int MT>
+    __device__ __forceinline__ bool take(Bars *S, uint32_t ring, int slot_bytes, int slots, bool active, int warp,
+                                         int lane, Frag<MT> &f) {
+        const int cs = s;
+        const uint32_t cph = ph;
+        if (++s == slots) {
+            s = 0;
+            ph ^= 1;
+        }
+        if (ok) ok = mbar_wait(&S->full[cs], cph, &g_timeouts);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return false;
+        if (active) {
+            const uint32_t chunk = ring + (uint32_t)cs * slot_bytes + warp * 16 * CH;
+            const int g = lane >> 2, t = lane & 3;
+            f.wa = lds_v4(chunk + w_off(g, t));
+            f.wb = lds_v4(chunk + w_off(g + 8, t));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S->empty[cs]);
+        return active;
+    }
+};
+
+// Producer side, one thread.
+struct Giver {
+    int s = 0;
+    uint32_t ph = 1;
+    uint32_t it = 0;
+    __device__ __forceinline__ bool give(Bars *S, uint8_t *ring, int slot_bytes, int slots, const CUtensorMap *tm,
+                                         int row, int chunk) {
+        if (!mbar_wait(&S->empty[s], ph, &g_timeouts) || *(volatile uint32_t *)&S->abort) return false;
+        mbar_arrive_expect_tx(&S->full[s], slot_bytes);
+        tma_load_3d(ring + (size_t)s * slot_bytes, tm, &S->full[s], 0, row, chunk);
+        if (++s == slots) {
+            s = 0;
+            ph ^= 1;
+        }
+        it++;
+        return true;
+    }
+    // wait out the copies still in flight so that none lands after exit
+    __device__ __forceinline__ void give_up(Bars *S, int slots) {
+        S->abort = 1;
+        for (uint32_t i = it > (uint32_t)slots ? it - slots : 0; i < it; i++)
+            mbar_wait(&S->full[i % slots], (i / slots) & 1, &g_timeouts);
+    }
+};
+
+__device__ __forceinline__ void init_bars(Bars *S, int slots) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < slots; s++) {
+            mbar_init(&S->full[s], 1);
+            mbar_init(&S->empty[s], kConsumers);
+        }
+        for (int m = 0; m < kMoeMaxTokens; m++) S->rowmax[m] = 0;
+        S->abort = 0;
+        fence_mbar_init();
     }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+// The sixteen warps' partial sums of `n` outputs (n = tiles x MT x 128; an
+// output's index is ((tile * MT + token half) * 4 + r) * 32 + lane, as the MMA
+// leaves it), added in warp order.
+template <int TG, int MT>
+__device__ __forceinline__ void reduce_warps(const float (&acc)[TG][MT][4], float *red, float *sums, int warp, int lane,
+                                             int n) {
+    consumers_sync();  // the previous group's sums have been read
+#pragma unroll
+    for (int u = 0; u < TG; u++)
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) red[(((warp * TG + u) * MT + i) * 4 + r) * 32 + lane] = acc[u][i][r];
+    consumers_sync();
+    for (int v = threadIdx.x; v < n; v += 32 * kConsumers) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; w++) sum += red[w * TG * MT * 128 + v];
+        sums[v] = sum;
+    }
+    consumers_sync();
 }
 
-__global__ void k_moe_gate_up(MoeArgs a, const Routing *R, float *act) {
-    const int lane = threadIdx.x & 31, pair = blockIdx.y;
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = pair / a.topk;
-    const int64_t e = R->id[pair];
-    const int hb = a.hidden >> 7;
-    float v[2];
-    for (int part = 0; part < 2; part++) {
-        const int64_t row = (2 * e + part) * a.inter + i;
-        float acc = 0.0f;
-        for (int k = lane; k < a.hidden; k += 32)
-            acc += bf16_bits_to_f32(a.x[(int64_t)t * a.hidden + k]) * e4m3_to_f32(a.w_gu[row * a.hidden + k]) *
-                   a.s_gu[(row >> 7) * hb + (k >> 7)];
-        v[part] = warp_sum(acc);
+// Workspace layout.
+struct Ws {
+    __half *act;       // [tokens * topk, inter], times a power of two per 16
+    uint8_t *act_exp;  // [tokens * topk, inter / 16]: exponent field of the 16 values' largest
+    int *count;        // [hidden / 32] shares of a tile that have come
+    float *part;       // [CTAs][2][kSums] FP32 sums of shared tiles
+};
+
+// The power of two for 16 (or a row of) act values whose largest has this
+// FP32 exponent field: brings it to [2^14, 2^15).
+__device__ __forceinline__ int exp_shift(int e) { return e == 0 ? 127 : min(14 - (e - 127), 127); }
+
+// ---------------------------------------------------------------- gate, up --
+//   tmW  [experts * 2 inter] rows x hidden, as (64 B, rows, hidden / 64), box
+//        (64, 16, ring.chunks)
+template <int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_moe_gate_up(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
+    constexpr int PG = MT == 1 ? 2 : 1, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int slot_bytes = ring.chunks * 16 * CH;
+    float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
+    float *sums = red + kConsumers * kSums;
+    Route *R = reinterpret_cast<Route *>(sums + kSums);
+    Bars *S = reinterpret_cast<Bars *>(R + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = a.hidden, I = a.inter, T = a.tokens;
+    init_bars(S, ring.slots);
+    __syncthreads();
+    dependency_wait();
+    // the down kernel may start where CTAs run out; it reads nothing that this
+    // one writes before it has completed, and everything before this one has
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // each token's largest magnitude, found by all consumer warps together
+    if (warp < kConsumers) {
+        constexpr int B = 8;
+        const int parts = kConsumers / T, m = warp % T, p = warp / T;
+        uint32_t mx = 0;
+        if (p < parts) {
+            const int units = H >> 3, per = (units + parts - 1) / parts;
+            const int u0 = p * per, u1 = min(units, u0 + per);
+            const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + (int64_t)m * H);
+            for (int u = u0 + lane; u < u1; u += 32 * B) {
+                uint4 v[B];
+#pragma unroll
+                for (int j = 0; j < B; j++) v[j] = u + 32 * j < u1 ? ldg_nc_v4(xr + u + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < B; j++)
+                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
+                                               __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
+            }
+        }
+        mx = max(mx & 0xFFFFu, mx >> 16);
+        mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+        if (lane == 0 && p < parts) atomicMax(&S->rowmax[m], mx);
     }
-    if (lane == 0) act[(int64_t)pair * a.inter + i] = v[0] / (1.0f + expf(-v[0])) * v[1];
+    route(a, R);
+
+    // this CTA's share of the (expert, 16 rows) units
+    const int per_expert = I >> 4;
+    const int64_t units = (int64_t)R->active * per_expert;
+    const int64_t u_begin = units * blockIdx.x / gridDim.x, u_end = units * (blockIdx.x + 1) / gridDim.x;
+
+    if (warp == kConsumers) {
+        if (elect_one()) {
+            prefetch_tensormap(&tmW);
+            Giver give;
+            bool ok = true;
+            for (int64_t u = u_begin; u < u_end && ok;) {
+                const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
+                const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
+                const int row = (int)R->expert[ai] * 2 * I + 16 * r;
+                for (int q = 0; q < ring.steps && ok; q++)
+                    for (int p = 0; p < 2 * n && ok; p++)  // gate, up, gate, up
+                        ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 16 * (p >> 1) + (p & 1) * I,
+                                       q * ring.chunks);
+                u += n;
+            }
+            if (!ok) give.give_up(S, ring.slots);
+        }
+        return;
+    }
+
+    if (blockIdx.x == 0) {
+        const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
+        if (t < T && j < a.topk) {
+            if (a.topk_ids) a.topk_ids[t * a.topk + j] = R->id[t][j];
+            if (a.topk_weights) a.topk_weights[t * a.topk + j] = R->weight[t][j];
+        }
+        for (int i = threadIdx.x; i < (H >> 5); i += 32 * kConsumers) ws.count[i] = 0;
+    }
+
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring_at = smem_u32(base);
+    const int hb = H >> 7;
+    const float xs0 = pow2i(row_shift(S->rowmax[g])), xs1 = MT == 2 ? pow2i(row_shift(S->rowmax[g + 8])) : 0.0f;
+    const uint16_t *x0 = a.x + (int64_t)min(g, T - 1) * H + CH * warp + 16 * t;
+    const uint16_t *x1 = a.x + (int64_t)min(g + 8, T - 1) * H + CH * warp + 16 * t;
+    // this lane's activation fragments of step q: zeros for a token that did
+    // not choose the expert, and past the end of K
+    auto load_x = [&](uint32_t mask, int q, uint4(&xa)[2], uint4(&xb)[2]) {
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        const int k = q * ring.chunks * CH;
+        const bool in = warp < ring.chunks && k + CH * warp < H;
+        const bool v0 = in && ((mask >> g) & 1);
+        xa[0] = v0 ? ldg_nc_v4(x0 + k) : z;
+        xa[1] = v0 ? ldg_nc_v4(x0 + k + 8) : z;
+        if (MT == 2) {
+            const bool v1 = in && ((mask >> (g + 8)) & 1);
+            xb[0] = v1 ? ldg_nc_v4(x1 + k) : z;
+            xb[1] = v1 ? ldg_nc_v4(x1 + k + 8) : z;
+        }
+    };
+    Taker take;
+    uint4 nxa[2], nxb[2];
+    if (u_begin < u_end) load_x(R->tokens[u_begin / per_expert], 0, nxa, nxb);
+    for (int64_t u = u_begin; u < u_end;) {
+        const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
+        const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
+        const uint32_t mask = R->tokens[ai];
+        const int64_t e = R->expert[ai];
+        // a unit's 16 rows lie in one scale block; the pairs of a group may not
+        const float *sg[PG], *su[PG];
+#pragma unroll
+        for (int p = 0; p < PG; p++) {
+            const int row = 16 * min(r + p, per_expert - 1);
+            sg[p] = a.s_gu + ((e * 2 * I + row) >> 7) * hb;
+            su[p] = a.s_gu + ((e * 2 * I + I + row) >> 7) * hb;
+        }
+        float acc[TG][MT][4] = {};
+        for (int q = 0; q < ring.steps; q++) {
+            Frag<MT> f;
+            x_to_f16<MT>(nxa, xs0, f.xa);
+            if (MT == 2) x_to_f16<MT>(nxb, xs1, f.xb);
+            if (q + 1 < ring.steps)
+                load_x(mask, q + 1, nxa, nxb);
+            else if (u + n < u_end)
+                load_x(R->tokens[(u + n) / per_expert], 0, nxa, nxb);
+            const int kc = (q * ring.chunks + warp) * CH;
+            const bool active = warp < ring.chunks && kc < H;
+            float sc[TG];
+#pragma unroll
+            for (int p = 0; p < PG; p++) {
+                sc[2 * p] = active ? __ldg(sg[p] + (kc >> 7)) : 0.0f;
+                sc[2 * p + 1] = active ? __ldg(su[p] + (kc >> 7)) : 0.0f;
+            }
+#pragma unroll
+            for (int v = 0; v < TG; v++) {
+                if (v >= 2 * n) break;
+                if (!take.take<MT>(S, ring_at, slot_bytes, ring.slots, active, warp, lane, f)) continue;
+                float d[MT][4] = {};
+                chunk_mma<MT>(d, f);
+#pragma unroll
+                for (int i = 0; i < MT; i++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++) acc[v][i][c] = __fmaf_rn(d[i][c], sc[v], acc[v][i][c]);
+            }
+        }
+        reduce_warps<TG, MT>(acc, red, sums, warp, lane, 2 * n * MT * 128);
+        // silu(gate) * up: a warp takes one (pair, token half, column parity),
+        // a lane rows g and g + 8 of token 8 i + 2 t + parity
+        if (warp < n * MT * 2) {
+            const int p = warp / (2 * MT), i = (warp >> 1) % MT, c = warp & 1;
+            const int m = 8 * i + 2 * t + c;
+            const float unscale = pow2i(-row_shift(S->rowmax[m]));
+            const float *gs = sums + ((2 * p * MT + i) * 4 + c) * 32 + lane, *us = gs + MT * 128;
+            float v[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const float gate = gs[64 * k] * unscale, up = us[64 * k] * unscale;
+                v[k] = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
+            }
+            float mx = fmaxf(fabsf(v[0]), fabsf(v[1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            if ((mask >> m) & 1) {
+                const int64_t pair = (int64_t)m * a.topk + R->pick[ai][m];
+                const int ex = (int)(__float_as_uint(mx) >> 23);
+                const float s = pow2i(exp_shift(ex));
+                __half *dst = ws.act + pair * I + 16 * (r + p) + g;
+                dst[0] = __float2half_rn(v[0] * s);
+                dst[8] = __float2half_rn(v[1] * s);
+                if (g == 0) ws.act_exp[pair * per_expert + r + p] = (uint8_t)ex;
+            }
+        }
+        u += n;
+    }
+    if (!take.ok && lane == 0) S->abort = 1;
 }
 
-__global__ void k_moe_down(MoeArgs a, const Routing *R, const float *act) {
-    const int lane = threadIdx.x & 31, t = blockIdx.y;
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int ib = a.inter >> 7;
-    float sum = 0.0f;
-    for (int j = 0; j < a.topk; j++) {
-        const int pair = t * a.topk + j;
-        const float p = R->weight[pair];
-        if (p == 0.0f) continue;
-        const int64_t row = (int64_t)R->id[pair] * a.hidden + n;
-        float acc = 0.0f;
-        for (int k = lane; k < a.inter; k += 32)
-            acc += act[(int64_t)pair * a.inter + k] * e4m3_to_f32(a.w_d[row * a.inter + k]) *
-                   a.s_d[(row >> 7) * ib + (k >> 7)];
-        sum += p * warp_sum(acc);
+// -------------------------------------------------------------------- down --
+//   tmW  [experts * hidden] rows x inter, as (64 B, rows, inter / 64), box
+//        (64, 16, ring.chunks)
+template <int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_moe_down(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
+    constexpr int TG = 2;  // 16-row tiles sharing one pass over act
+    constexpr int OUTS = TG * MT * 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int slot_bytes = ring.chunks * 16 * CH;
+    float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
+    float *sums = red + kConsumers * kSums;
+    float *coef = sums + kSums;  // [active][tokens]: routing weight x the undone power of two
+    Route *R = reinterpret_cast<Route *>(coef + kMaxActive * kMoeMaxTokens);
+    Bars *S = reinterpret_cast<Bars *>(R + 1);
+    int8_t *shift = reinterpret_cast<int8_t *>(S + 1);  // [active][tokens]: the row's power of two
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = a.hidden, I = a.inter, T = a.tokens;
+    init_bars(S, ring.slots);
+    __syncthreads();
+    route(a, R);  // the logits were there before the previous kernel started
+
+    // this CTA's share of the (32-row tile, expert, K step) sequence
+    const int64_t steps = (int64_t)R->active * ring.steps;  // of one tile
+    const int64_t all = steps * (H >> 5);
+    // no share is empty: the count of a shared tile's shares relies on it
+    const int64_t shares = min((int64_t)gridDim.x, max(all, (int64_t)1));
+    const int64_t u_begin = min(all, all * blockIdx.x / shares), u_end = min(all, all * (blockIdx.x + 1) / shares);
+
+    if (warp == kConsumers) {
+        if (elect_one()) {
+            prefetch_tensormap(&tmW);
+            Giver give;
+            bool ok = true;
+            int tile = steps ? (int)(u_begin / steps) : 0;
+            int64_t st = steps ? u_begin - tile * steps : 0;
+            int ai = (int)(st / ring.steps), q = (int)(st - (int64_t)ai * ring.steps);
+            for (int64_t u = u_begin; u < u_end && ok; u++) {
+                const int row = (int)R->expert[ai] * H + 32 * tile;
+                for (int v = 0; v < TG && ok; v++)
+                    ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 16 * v, q * ring.chunks);
+                if (++q == ring.steps) {
+                    q = 0;
+                    if (++ai == R->active) {
+                        ai = 0;
+                        tile++;
+                    }
+                }
+            }
+            if (!ok) give.give_up(S, ring.slots);
+            dependency_wait();  // no CTA ends before the previous kernel has
+        }
+        return;
     }
-    if (lane == 0) a.out[(int64_t)t * a.hidden + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+
+    dependency_wait();
+    if (all == 0) {  // no token has an expert
+        for (int64_t i = (int64_t)blockIdx.x * 32 * kConsumers + threadIdx.x; i < (int64_t)T * H;
+             i += (int64_t)gridDim.x * 32 * kConsumers)
+            a.out[i] = 0;
+        return;
+    }
+    // every (token, choice)'s power of two, from its groups' exponents
+    for (int p = warp; p < T * a.topk; p += kConsumers) {
+        const int m = p / a.topk, j = p - m * a.topk;
+        const float w = R->weight[m][j];
+        if (!(w > 0.0f)) continue;
+        const uint2 *ex = reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)p * (I >> 4));
+        uint32_t mx = 0;
+        for (int i = lane; i < (I >> 7); i += 32) {
+            const uint2 v = __ldcg(ex + i);
+            mx = __vmaxu4(mx, __vmaxu4(v.x, v.y));
+        }
+        mx = __vmaxu4(mx, mx >> 16);
+        mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu));
+        if (lane == 0) {
+            const int s = exp_shift((int)mx), at = (int)R->slot[R->id[m][j]] * kMoeMaxTokens + m;
+            shift[at] = (int8_t)s;
+            coef[at] = w * pow2i(-s);
+        }
+    }
+    consumers_sync();
+
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring_at = smem_u32(base);
+    const int hb = H >> 7, ib = I >> 7;
+    struct Next {
+        uint4 v[2];
+        int ex;  // -1: no such token here
+    };
+    // act of token m for expert place ai at K offset k: sixteen FP16 values
+    // and their group's exponent
+    auto load_act = [&](int ai, int m, int k, bool in, Next &o) {
+        in = in && ((R->tokens[ai] >> m) & 1);
+        o.v[0] = o.v[1] = make_uint4(0u, 0u, 0u, 0u);
+        o.ex = -1;
+        if (in) {
+            const int64_t pair = (int64_t)m * a.topk + R->pick[ai][m];
+            const uint4 *src = reinterpret_cast<const uint4 *>(ws.act + pair * I + k);
+            o.v[0] = __ldcg(src);
+            o.v[1] = __ldcg(src + 1);
+            o.ex = __ldcg(ws.act_exp + pair * (I >> 4) + (k >> 4));
+        }
+    };
+    // brought to the row's power of two: a factor of 2^-d, exact down to
+    // FP16's subnormals
+    auto to_row = [&](const Next &n, int row_shift_, uint32_t(&o)[8]) {
+        const int d = n.ex < 0 ? 25 : exp_shift(n.ex) - row_shift_;  // >= 0
+        const __half f = d > 24 ? __ushort_as_half((unsigned short)0)
+                                : (d <= 14 ? __ushort_as_half((unsigned short)((15 - d) << 10))
+                                           : __ushort_as_half((unsigned short)(1 << (24 - d))));
+        const __half2 f2 = __half2half2(f);
+        const uint32_t w[8] = {n.v[0].x, n.v[0].y, n.v[0].z, n.v[0].w, n.v[1].x, n.v[1].y, n.v[1].z, n.v[1].w};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&w[j]), f2);
+            o[j] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    };
+    auto load_step = [&](int ai, int tile, int q, Next &n0, Next &n1, float &sc) {
+        const int kc = (q * ring.chunks + warp) * CH;
+        const bool in = warp < ring.chunks && kc < I;
+        load_act(ai, g, kc + 16 * t, in, n0);
+        if (MT == 2) load_act(ai, g + 8, kc + 16 * t, in, n1);
+        // the tile's 32 rows lie in one scale block
+        sc = in ? __ldg(a.s_d + ((int64_t)R->expert[ai] * hb + (tile >> 2)) * ib + (kc >> 7)) : 0.0f;
+    };
+
+    Taker take;
+    int tile = (int)(u_begin / steps);
+    int64_t st = u_begin - tile * steps;
+    int ai = (int)(st / ring.steps), q = (int)(st - (int64_t)ai * ring.steps);
+    Next n0, n1;
+    float sc_next = 0.0f;
+    if (u_begin < u_end) load_step(ai, tile, q, n0, n1, sc_next);
+    for (int64_t u = u_begin; u < u_end;) {
+        const int64_t first = st;
+        const int64_t count = min(steps - st, u_end - u);
+        float acc[TG][MT][4] = {};
+        for (int64_t k = 0; k < count; k++) {
+            Frag<MT> f;
+            const int8_t *sh = shift + ai * kMoeMaxTokens;
+            to_row(n0, sh[g], f.xa);
+            if (MT == 2) to_row(n1, sh[g + 8], f.xb);
+            const float sc = sc_next;
+            float cf[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const int m = 8 * i + 2 * t + c;
+                    cf[i][c] = ((R->tokens[ai] >> m) & 1) ? coef[ai * kMoeMaxTokens + m] * sc : 0.0f;
+                }
+            const bool active = warp < ring.chunks && (q * ring.chunks + warp) * CH < I;
+            int tile1 = tile;
+            if (++q == ring.steps) {
+                q = 0;
+                if (++ai == R->active) {
+                    ai = 0;
+                    tile1++;
+                }
+            }
+            if (u + k + 1 < u_end) load_step(ai, tile1, q, n0, n1, sc_next);
+#pragma unroll
+            for (int v = 0; v < TG; v++) {
+                if (!take.take<MT>(S, ring_at, slot_bytes, ring.slots, active, warp, lane, f)) continue;
+                float d[MT][4] = {};
+                chunk_mma<MT>(d, f);
+#pragma unroll
+                for (int i = 0; i < MT; i++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++) acc[v][i][c] = __fmaf_rn(d[i][c], cf[i][c & 1], acc[v][i][c]);
+            }
+        }
+        reduce_warps<TG, MT>(acc, red, sums, warp, lane, OUTS);
+        u += count;
+        st += count;
+        bool finish = true;
+        int b0 = 0, b1 = 0;
+        if (first != 0 || st != steps) {
+            // a shared tile: leave the sums, count, and add everybody's if last
+            const int64_t t0 = (int64_t)tile * steps;
+            b0 = (int)(((t0 + 1) * shares - 1) / all);
+            b1 = (int)(((t0 + steps) * shares - 1) / all);
+            float *mine = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kSums;
+            for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) __stcg(mine + v, sums[v]);
+            __threadfence();
+            consumers_sync();
+            if (threadIdx.x == 0) S->last = atomicAdd(ws.count + tile, 1) == b1 - b0;
+            consumers_sync();
+            finish = S->last != 0;
+            if (finish) __threadfence();
+        }
+        if (finish) {
+            for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) {
+                float sum = sums[v];
+                if (b1 > b0) {
+                    sum = 0.0f;
+                    for (int b = b0; b <= b1; b++) {
+                        // a share's slot: 1 where it starts at the tile's first step
+                        const int64_t begin = all * b / shares;
+                        const int head = begin <= (int64_t)tile * steps;
+                        sum += __ldcg(ws.part + ((int64_t)b * 2 + head) * kSums + v);
+                    }
+                }
+                const int w = v / (MT * 128), i = (v >> 7) % MT, r = (v >> 5) & 3, ln = v & 31;
+                const int n = 32 * tile + 16 * w + (ln >> 2) + 8 * (r >> 1), m = 8 * i + 2 * (ln & 3) + (r & 1);
+                if (m < T) a.out[(int64_t)m * H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+            }
+        }
+        if (st == steps) {
+            st = 0;
+            tile++;
+        }
+    }
+    if (!take.ok && lane == 0) S->abort = 1;
+}
+
+// -------------------------------------------------------------------- host --
+
+constexpr size_t kSmemMax = 232448;
+constexpr size_t gate_up_fixed() { return 1024 + (kConsumers + 1) * kSums * 4 + sizeof(Route) + sizeof(Bars); }
+constexpr size_t down_fixed() {
+    return gate_up_fixed() + (size_t)kMaxActive * kMoeMaxTokens * (sizeof(float) + 1);
+}
+
+// Boxes of equal size, at most 1 KB of K, and as many as fit.
+Ring ring_for(int k, size_t fixed) {
+    Ring r;
+    const int chunks = k / CH;
+    r.steps = (chunks + 15) / 16;
+    r.chunks = (chunks + r.steps - 1) / r.steps;
+    const int room = (int)((kSmemMax - fixed) / ((size_t)r.chunks * 16 * CH));
+    r.slots = room < kMaxSlots ? room : kMaxSlots;
+    return r;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
+    const size_t pairs = (size_t)tokens * topk;
+    const size_t act = align256(pairs * inter * sizeof(__half)), ex = align256(pairs * (inter / 16)),
+                 count = align256((size_t)hidden / 32 * sizeof(int)),
+                 part = (size_t)sm_count() * 2 * kSums * sizeof(float);
+    if (ws) {
+        uint8_t *b = static_cast<uint8_t *>(p);
+        ws->act = reinterpret_cast<__half *>(b);
+        ws->act_exp = b + act;
+        ws->count = reinterpret_cast<int *>(b + act + ex);
+        ws->part = reinterpret_cast<float *>(b + act + ex + count);
+    }
+    return act + ex + count + part;
+}
+
+template <class F>
+cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Ring &ring, size_t smem, const MoeArgs &a,
+                       const Ws &ws, cudaStream_t s) {
+    alignas(64) CUtensorMap tm;
+    const uint64_t d[3] = {CH, (uint64_t)rows, (uint64_t)k / CH}, st[2] = {(uint64_t)k, CH};
+    const uint32_t box[3] = {CH, 16, (uint32_t)ring.chunks};
+    if (!make_tmap(&tm, w, 1, 3, d, st, box, 64)) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sm_count());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tm, a, ring, ws);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+template <int MT> cudaError_t launch_mt(const MoeArgs &a, cudaStream_t s) {
+    static DeviceOnce attrs;
+    cudaError_t e = attrs.run([] {
+        const cudaError_t err = cudaFuncSetAttribute(k_moe_gate_up<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     (int)kSmemMax);
+        if (err != cudaSuccess) return err;
+        return cudaFuncSetAttribute(k_moe_down<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    });
+    if (e != cudaSuccess) return e;
+    Ws ws;
+    ws_layout(a.workspace, a.tokens, a.hidden, a.inter, a.topk, &ws);
+    const Ring up = ring_for(a.hidden, gate_up_fixed()), down = ring_for(a.inter, down_fixed());
+    e = launch_one(k_moe_gate_up<MT>, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, up,
+                   gate_up_fixed() + (size_t)up.slots * up.chunks * 16 * CH, a, ws, s);
+    if (e != cudaSuccess) return e;
+    return launch_one(k_moe_down<MT>, a.w_d, (int64_t)a.experts * a.hidden, a.inter, down,
+                      down_fixed() + (size_t)down.slots * down.chunks * 16 * CH, a, ws, s);
 }
 
 }  // namespace
 
+uint32_t take_timeouts_moe() {
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+    cudaMemcpyToSymbol(g_timeouts, &zero, sizeof(zero));
+    return v;
+}
+
 size_t fp8_moe_workspace_bytes(int tokens, int hidden, int inter, int topk) {
-    (void)hidden;
-    return ((sizeof(Routing) + 255) & ~size_t(255)) + (size_t)tokens * topk * inter * sizeof(float);
+    return ws_layout(nullptr, tokens, hidden, inter, topk, nullptr);
 }
 
 cudaError_t launch_fp8_moe_blockscaled(const MoeArgs &a, cudaStream_t s) {
-    Routing *R = static_cast<Routing *>(a.workspace);
-    float *act = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + ((sizeof(Routing) + 255) & ~size_t(255)));
-    k_moe_route<<<1, 32 * a.tokens, 0, s>>>(a, R);
-    k_moe_gate_up<<<dim3(a.inter / 8, a.tokens * a.topk), 256, 0, s>>>(a, R, act);
-    k_moe_down<<<dim3(a.hidden / 8, a.tokens), 256, 0, s>>>(a, R, act);
-    note_launch();
-    note_launch();
-    note_launch();
-    return cudaGetLastError();
+    return a.tokens <= 8 ? launch_mt<1>(a, s) : launch_mt<2>(a, s);
 }
 
 }  // namespace bsq
