@@ -6,10 +6,10 @@
 //
 // The reached experts' weights, read once, are the whole cost, so both kernels
 // are streaming reads built like the FP8 GEMV: one CTA per SM, a TMA producer
-// warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, and
-// sixteen consumer warps that split a box's K into 64-byte chunks (E4M3 ->
-// FP16 exactly, FP16 MMAs with FP32 sums, each chunk's sum times its block
-// scale).  The MMA's eight (or sixteen) columns are the tokens themselves: a
+// warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, two
+// boxes to a slot, and eight consumer warps that split a box's K into its
+// 128-wide scale blocks (E4M3 -> FP16 exactly, FP16 MMAs with FP32 sums, each
+// block's sum times its scale).  The MMA's eight (or sixteen) columns are the tokens themselves: a
 // token that did not choose the expert has zeros there, which costs nothing
 // beside the stream, and no gather or scatter is needed.
 //
@@ -43,11 +43,18 @@ namespace {
 
 using namespace gv;
 
-constexpr int kConsumers = 16;
+// Eight consumer warps, so that each has the registers to run a slot's boxes
+// as independent chains of MMAs (sixteen warps of half the work took 600
+// cycles per box, more than the 700 that the stream leaves for two).
+constexpr int kConsumers = 8;
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kMaxSlots = 24;
+constexpr int SB = 128;        // K of one scale block: two 64-byte chunks
+constexpr int kMaxSlots = 16;
 constexpr int kMaxActive = kMoeMaxTokens * kMoeMaxTopk;
-constexpr int kSums = 512;  // output sums of a group: tiles x (8 or 16 tokens) x 16 rows, at most
+constexpr int kRed = 8192;     // floats of the warps' partial sums; the routing keys before that
+constexpr int kSums = 1024;    // floats of a group's sums: tiles x (8 or 16 tokens) x 16 rows, at most
+constexpr int kPart = 512;     // the down kernel's
+static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums, "shared buffer");
 
 static __device__ unsigned int g_timeouts;
 
@@ -58,7 +65,7 @@ struct alignas(16) Route {
     uint16_t expert[kMaxActive];        // the reached experts, in order
     uint16_t tokens[kMaxActive];        // their tokens, a bit each
     uint8_t pick[kMaxActive][kMoeMaxTokens];  // which of the token's choices the expert is
-    int warp_count[kConsumers];
+    int warp_count[kMoeMaxExperts / 32];
     int active;
 };
 
@@ -70,10 +77,10 @@ struct alignas(16) Bars {
     uint32_t last;  // this CTA finishes the tile
 };
 
-// Box geometry: `chunks` 64-byte chunks of K per box, `steps` boxes along K,
-// `slots` boxes in the ring.
+// Ring geometry: a slot holds two boxes of 16 weight rows x `blocks` scale
+// blocks of K; `steps` slots along K, `slots` in the ring.
 struct Ring {
-    int chunks, steps, slots;
+    int blocks, steps, slots;
 };
 
 __device__ __forceinline__ void consumers_sync() {
@@ -99,121 +106,175 @@ __device__ __forceinline__ float route_exp(float l, float mx) {
     return l == mx ? 1.0f : expf(l - mx);
 }
 
-// Routes every token (one warp each) and lists the reached experts.  Called
-// by all threads of the CTA.
-__device__ __forceinline__ void route(const MoeArgs &a, Route *R) {
-    constexpr int PER = kMoeMaxExperts / 32;
+// Routes every token (a warp each, in turn) and lists the reached experts.
+// `keys`: kMoeMaxTokens x kMoeMaxExperts words.  Called by all threads of the
+// CTA.
+__device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t key[PER];
-    if (warp < a.tokens) {
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            const int e = lane + 32 * i;
-            key[i] = e < a.experts ? logit_key(__ldg(a.logits + (int64_t)warp * a.experts + e)) : 0u;
-        }
-    }
     for (int e = threadIdx.x; e < kMoeMaxExperts; e += kThreads) R->slot[e] = 0;
     __syncthreads();
-    if (warp < a.tokens) {
-        uint32_t taken = 0;
-        float mx = 0.0f, sum = 0.0f, mine = 0.0f;
+    for (int t = warp; t < a.tokens; t += kThreads / 32) {
+        // each lane's largest key and its lowest index
+        uint32_t *key = keys + t * kMoeMaxExperts;
+        uint32_t best = 0;
+        int at = lane;
+        for (int e = lane; e < a.experts; e += 32) {
+            const uint32_t k = logit_key(__ldg(a.logits + (int64_t)t * a.experts + e));
+            key[e] = k;
+            if (k > best) {
+                best = k;
+                at = e;
+            }
+        }
+        const float mx = key_logit(__reduce_max_sync(0xFFFFFFFFu, best));
+        float sum = 0.0f, mine = 0.0f;
         int my_id = 0;
+        if (!a.renormalise) {
+            for (int e = lane; e < a.experts; e += 32) sum += route_exp(key_logit(key[e]), mx);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        }
         for (int j = 0; j < a.topk; j++) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < PER; i++)
-                if (32 * i < a.experts && !((taken >> i) & 1)) best = max(best, key[i]);
-            best = __reduce_max_sync(0xFFFFFFFFu, best);
-            int e = kMoeMaxExperts - 1;
-#pragma unroll
-            for (int i = PER - 1; i >= 0; i--)
-                if (32 * i < a.experts && !((taken >> i) & 1) && key[i] == best && lane + 32 * i < a.experts)
-                    e = lane + 32 * i;
-            e = __reduce_min_sync(0xFFFFFFFFu, e);
-            if ((e & 31) == lane) taken |= 1u << (e >> 5);
-            const float l = key_logit(best);
-            if (j == 0) mx = l;
-            const float p = route_exp(l, mx);
-            sum += p;
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+            const int e = __reduce_min_sync(0xFFFFFFFFu, best == top ? at : kMoeMaxExperts);
+            const float p = route_exp(key_logit(top), mx);
+            if (a.renormalise) sum += p;
             if (lane == j) {
                 mine = p;
                 my_id = e;
             }
-        }
-        if (!a.renormalise) {
-            sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER; i++)
-                if (lane + 32 * i < a.experts) sum += route_exp(key_logit(key[i]), mx);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if ((e & 31) == lane) {  // its owner looks for its next
+                key[e] = 0;
+                best = 0;
+                for (int i = lane; i < a.experts; i += 32) {
+                    const uint32_t k = key[i];
+                    if (k > best) {
+                        best = k;
+                        at = i;
+                    }
+                }
+            }
+            __syncwarp();
         }
         if (lane < a.topk) {
             const float w = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;
-            R->id[warp][lane] = (uint16_t)my_id;
-            R->weight[warp][lane] = w;
+            R->id[t][lane] = (uint16_t)my_id;
+            R->weight[t][lane] = w;
             // an expert that adds nothing is not read
-            if (w > 0.0f) atomicOr(&R->slot[my_id], 1u << warp);
+            if (w > 0.0f) atomicOr(&R->slot[my_id], 1u << t);
         }
     }
     __syncthreads();
-    uint32_t mask = 0, ballot = 0;
+    constexpr int HALVES = kMoeMaxExperts / (32 * kConsumers);
+    uint32_t mask[HALVES], ballot[HALVES];
     if (warp < kConsumers) {
-        mask = R->slot[threadIdx.x];
-        ballot = __ballot_sync(0xFFFFFFFFu, mask != 0);
-        if (lane == 0) R->warp_count[warp] = __popc(ballot);
+#pragma unroll
+        for (int i = 0; i < HALVES; i++) {
+            mask[i] = R->slot[i * 32 * kConsumers + threadIdx.x];
+            ballot[i] = __ballot_sync(0xFFFFFFFFu, mask[i] != 0);
+            if (lane == 0) R->warp_count[i * kConsumers + warp] = __popc(ballot[i]);
+        }
     }
     __syncthreads();
     if (warp < kConsumers) {
-        int at = __popc(ballot & ((1u << lane) - 1u));
-        for (int w = 0; w < warp; w++) at += R->warp_count[w];
-        if (mask) {
-            R->expert[at] = (uint16_t)threadIdx.x;
-            R->tokens[at] = (uint16_t)mask;
-            R->slot[threadIdx.x] = at;
+#pragma unroll
+        for (int i = 0; i < HALVES; i++) {
+            const int w = i * kConsumers + warp, e = i * 32 * kConsumers + (int)threadIdx.x;
+            const int before = lane < w ? R->warp_count[lane] : 0;  // (at most 16 warps' counts)
+            const int at = (int)__reduce_add_sync(0xFFFFFFFFu, before) + __popc(ballot[i] & ((1u << lane) - 1u));
+            if (mask[i]) {
+                R->expert[at] = (uint16_t)e;
+                R->tokens[at] = (uint16_t)mask[i];
+                R->slot[e] = at;
+            }
+            if (e == kMoeMaxExperts - 1) R->active = at + (mask[i] != 0);
         }
-        if (threadIdx.x == 32 * kConsumers - 1) R->active = at + (mask != 0);
     }
     __syncthreads();
     const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
     if (t < a.tokens && j < a.topk && R->weight[t][j] > 0.0f) R->pick[R->slot[R->id[t][j]]][t] = (uint8_t)j;
     __syncthreads();
 }
-static_assert(32 * kConsumers == kMoeMaxExperts && kMoeMaxTopk == 16, "one thread per expert, 16 choices");
+static_assert(kMoeMaxExperts % (32 * kConsumers) == 0 && kMoeMaxExperts / 32 <= 32 && kMoeMaxTopk == 16 &&
+                  32 * kConsumers >= kMoeMaxTokens * kMoeMaxTopk,
+              "routing by one CTA");
 
 // ------------------------------------------------------------------- ring --
 
-// Consumer side of the ring: every consumer warp takes every box.
+// Bounded wait that sets the abort flag when it runs out, and returns without
+// waiting once that flag is set: the warps then reach the end of their loops
+// and barriers together, without a vote in the loop.
+__device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, Bars *S) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*(volatile uint32_t *)&S->abort) return;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(&g_timeouts, 1u);
+            *(volatile uint32_t *)&S->abort = 1;
+            return;
+        }
+    }
+}
+
+// Consumer side of the ring: every consumer warp takes its part of every slot.
 struct Taker {
     int s = 0;
     uint32_t ph = 0;
-    bool ok = true;
-    // The chunk of this warp in the next box (f.wa, f.wb), and the box given
-    // back.  After a timeout the warp keeps its loop and barrier sequence (so
-    // no other warp waits on it) but touches no slot.
-    template <int MT>
-    __device__ __forceinline__ bool take(Bars *S, uint32_t ring, int slot_bytes, int slots, bool active, int warp,
-                                         int lane, Frag<MT> &f) {
-        const int cs = s;
-        const uint32_t cph = ph;
+    uint32_t empty0;  // the give-back barriers, by cluster address (the plain form of the arrival
+                      // waits some 160 cycles for the warp's other memory operations)
+    __device__ __forceinline__ Taker(Bars *S) : empty0(mapa_shared(smem_u32(&S->empty[0]), 0)) {}
+    // Waits for the next slot; returns its address in shared memory.
+    __device__ __forceinline__ uint32_t take(Bars *S, uint32_t ring, int slot_bytes) {
+        wait_or_abort(&S->full[s], ph, S);
+        __syncwarp();
+        return ring + (uint32_t)s * slot_bytes;
+    }
+    // Gives it back.
+    __device__ __forceinline__ void give_back(int slots, int lane) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(empty0 + 8 * s);
         if (++s == slots) {
             s = 0;
             ph ^= 1;
         }
-        if (ok) ok = mbar_wait(&S->full[cs], cph, &g_timeouts);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return false;
-        if (active) {
-            const uint32_t chunk = ring + (uint32_t)cs * slot_bytes + warp * 16 * CH;
-            const int g = lane >> 2, t = lane & 3;
-            f.wa = lds_v4(chunk + w_off(g, t));
-            f.wb = lds_v4(chunk + w_off(g + 8, t));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S->empty[cs]);
-        return active;
     }
 };
+
+// The next slot: this warp's scale block (two chunks) of each of its two boxes
+// times the activation fragments f[0], f[1], as two independent chains of
+// MMAs, handed to `add` with its accumulator.
+template <int MT, class Add>
+__device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, int slot_bytes, int slots, bool active,
+                                         int warp, int lane, Frag<MT> (&f)[2], float (&acc0)[MT][4],
+                                         float (&acc1)[MT][4], Add &&add) {
+    const uint32_t at = take.take(S, ring, slot_bytes) + warp * 2 * 16 * CH;
+    const int g = lane >> 2, t = lane & 3;
+    uint4 w[2][2][2];  // [box][chunk][row g, g + 8]
+    if (active) {
+#pragma unroll
+        for (int v = 0; v < 2; v++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const uint32_t chunk = at + v * (slot_bytes >> 1) + c * 16 * CH;
+                w[v][c][0] = lds_v4(chunk + w_off(g, t));
+                w[v][c][1] = lds_v4(chunk + w_off(g + 8, t));
+            }
+    }
+    take.give_back(slots, lane);
+    if (!active) return;
+    float d[2][MT][4] = {};
+#pragma unroll
+    for (int c = 0; c < 2; c++)
+#pragma unroll
+        for (int v = 0; v < 2; v++) {
+            f[c].wa = w[v][c][0];
+            f[c].wb = w[v][c][1];
+            chunk_mma<MT>(d[v], f[c]);
+        }
+    add(acc0, d[0], 0);
+    add(acc1, d[1], 1);
+}
 
 // Producer side, one thread.
 struct Giver {
@@ -221,10 +282,11 @@ struct Giver {
     uint32_t ph = 1;
     uint32_t it = 0;
     __device__ __forceinline__ bool give(Bars *S, uint8_t *ring, int slot_bytes, int slots, const CUtensorMap *tm,
-                                         int row, int chunk) {
+                                         int row0, int row1, int chunk) {
         if (!mbar_wait(&S->empty[s], ph, &g_timeouts) || *(volatile uint32_t *)&S->abort) return false;
         mbar_arrive_expect_tx(&S->full[s], slot_bytes);
-        tma_load_3d(ring + (size_t)s * slot_bytes, tm, &S->full[s], 0, row, chunk);
+        tma_load_3d(ring + (size_t)s * slot_bytes, tm, &S->full[s], 0, row0, chunk);
+        tma_load_3d(ring + (size_t)s * slot_bytes + (slot_bytes >> 1), tm, &S->full[s], 0, row1, chunk);
         if (++s == slots) {
             s = 0;
             ph ^= 1;
@@ -252,7 +314,7 @@ __device__ __forceinline__ void init_bars(Bars *S, int slots) {
     }
 }
 
-// The sixteen warps' partial sums of `n` outputs (n = tiles x MT x 128; an
+// The warps' partial sums of `n` outputs (n = tiles x MT x 128; an
 // output's index is ((tile * MT + token half) * 4 + r) * 32 + lane, as the MMA
 // leaves it), added in warp order.
 template <int TG, int MT>
@@ -280,7 +342,7 @@ struct Ws {
     __half *act;       // [tokens * topk, inter], times a power of two per 16
     uint8_t *act_exp;  // [tokens * topk, inter / 16]: exponent field of the 16 values' largest
     int *count;        // [hidden / 32] shares of a tile that have come
-    float *part;       // [CTAs][2][kSums] FP32 sums of shared tiles
+    float *part;       // [CTAs][2][kPart] FP32 sums of shared tiles
 };
 
 // The power of two for 16 (or a row of) act values whose largest has this
@@ -289,16 +351,16 @@ __device__ __forceinline__ int exp_shift(int e) { return e == 0 ? 127 : min(14 -
 
 // ---------------------------------------------------------------- gate, up --
 //   tmW  [experts * 2 inter] rows x hidden, as (64 B, rows, hidden / 64), box
-//        (64, 16, ring.chunks)
+//        (64, 16, 2 ring.blocks)
 template <int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_gate_up(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
-    constexpr int PG = MT == 1 ? 2 : 1, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
+    constexpr int PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int slot_bytes = ring.chunks * 16 * CH;
+    const int slot_bytes = 2 * ring.blocks * 16 * SB;
     float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
-    float *sums = red + kConsumers * kSums;
+    float *sums = red + kRed;
     Route *R = reinterpret_cast<Route *>(sums + kSums);
     Bars *S = reinterpret_cast<Bars *>(R + 1);
 
@@ -311,30 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one writes before it has completed, and everything before this one has
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // each token's largest magnitude, found by all consumer warps together
-    if (warp < kConsumers) {
-        constexpr int B = 8;
-        const int parts = kConsumers / T, m = warp % T, p = warp / T;
-        uint32_t mx = 0;
-        if (p < parts) {
-            const int units = H >> 3, per = (units + parts - 1) / parts;
-            const int u0 = p * per, u1 = min(units, u0 + per);
-            const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + (int64_t)m * H);
-            for (int u = u0 + lane; u < u1; u += 32 * B) {
-                uint4 v[B];
-#pragma unroll
-                for (int j = 0; j < B; j++) v[j] = u + 32 * j < u1 ? ldg_nc_v4(xr + u + 32 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < B; j++)
-                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
-                                               __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
-            }
-        }
-        mx = max(mx & 0xFFFFu, mx >> 16);
-        mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-        if (lane == 0 && p < parts) atomicMax(&S->rowmax[m], mx);
-    }
-    route(a, R);
+    route(a, R, reinterpret_cast<uint32_t *>(red));
 
     // this CTA's share of the (expert, 16 rows) units
     const int per_expert = I >> 4;
@@ -351,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
                 const int row = (int)R->expert[ai] * 2 * I + 16 * r;
                 for (int q = 0; q < ring.steps && ok; q++)
-                    for (int p = 0; p < 2 * n && ok; p++)  // gate, up, gate, up
-                        ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 16 * (p >> 1) + (p & 1) * I,
-                                       q * ring.chunks);
+                    for (int p = 0; p < n && ok; p++)
+                        ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 16 * p, row + 16 * p + I,
+                                       q * ring.blocks * 2);
                 u += n;
             }
             if (!ok) give.give_up(S, ring.slots);
@@ -361,6 +400,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
+    // each token's largest magnitude, found by all consumer warps together (the
+    // first weight copies are on their way)
+    {
+        constexpr int B = 8;
+        const int parts = T < kConsumers ? kConsumers / T : 1;
+        const int units = H >> 3, per = (units + parts - 1) / parts;
+        for (int task = warp; task < T * parts; task += kConsumers) {
+            const int m = task % T, p = task / T;
+            const int u0 = p * per, u1 = min(units, u0 + per);
+            const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + (int64_t)m * H);
+            uint32_t mx = 0;
+            for (int u = u0 + lane; u < u1; u += 32 * B) {
+                uint4 v[B];
+#pragma unroll
+                for (int j = 0; j < B; j++) v[j] = u + 32 * j < u1 ? ldg_nc_v4(xr + u + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < B; j++)
+                    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu),
+                                               __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu)));
+            }
+            mx = max(mx & 0xFFFFu, mx >> 16);
+            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+            if (lane == 0) atomicMax(&S->rowmax[m], mx);
+        }
+    }
     if (blockIdx.x == 0) {
         const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
         if (t < T && j < a.topk) {
@@ -369,71 +433,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = threadIdx.x; i < (H >> 5); i += 32 * kConsumers) ws.count[i] = 0;
     }
+    consumers_sync();
 
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7;
     const float xs0 = pow2i(row_shift(S->rowmax[g])), xs1 = MT == 2 ? pow2i(row_shift(S->rowmax[g + 8])) : 0.0f;
-    const uint16_t *x0 = a.x + (int64_t)min(g, T - 1) * H + CH * warp + 16 * t;
-    const uint16_t *x1 = a.x + (int64_t)min(g + 8, T - 1) * H + CH * warp + 16 * t;
-    // this lane's activation fragments of step q: zeros for a token that did
-    // not choose the expert, and past the end of K
-    auto load_x = [&](uint32_t mask, int q, uint4(&xa)[2], uint4(&xb)[2]) {
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        const int k = q * ring.chunks * CH;
-        const bool in = warp < ring.chunks && k + CH * warp < H;
-        const bool v0 = in && ((mask >> g) & 1);
-        xa[0] = v0 ? ldg_nc_v4(x0 + k) : z;
-        xa[1] = v0 ? ldg_nc_v4(x0 + k + 8) : z;
-        if (MT == 2) {
-            const bool v1 = in && ((mask >> (g + 8)) & 1);
-            xb[0] = v1 ? ldg_nc_v4(x1 + k) : z;
-            xb[1] = v1 ? ldg_nc_v4(x1 + k + 8) : z;
+    const uint16_t *x0 = a.x + (int64_t)min(g, T - 1) * H + SB * warp + 16 * t;
+    const uint16_t *x1 = a.x + (int64_t)min(g + 8, T - 1) * H + SB * warp + 16 * t;
+    // this lane's activations of step q, [chunk][token half][16-byte half]:
+    // zeros for a token that did not choose the expert, and past the end of K
+    auto load_x = [&](uint32_t mask, int q, uint4(&x)[2][MT][2]) {
+        const int k = q * ring.blocks * SB;
+        const bool in = warp < ring.blocks && k + SB * warp < H;
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int i = 0; i < MT; i++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    x[c][i][h] = in && ((mask >> (g + 8 * i)) & 1) ? ldg_nc_v4((i ? x1 : x0) + k + CH * c + 8 * h)
+                                                                   : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // the scales of this warp's block of step q for the tiles of the group at
+    // unit u (a unit's 16 rows lie in one scale block; a group's may not)
+    auto load_scales = [&](int64_t u, int q, float(&sc)[TG]) {
+        const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
+        const int kb = q * ring.blocks + warp;
+        const bool in = warp < ring.blocks && kb < hb;
+#pragma unroll
+        for (int p = 0; p < PG; p++) {
+            const int64_t row = (int64_t)R->expert[ai] * 2 * I + 16 * min(r + p, per_expert - 1);
+            const float *s = a.s_gu + (row >> 7) * hb + kb;
+            sc[2 * p] = in ? __ldg(s) : 0.0f;
+            sc[2 * p + 1] = in ? __ldg(s + (int64_t)(I >> 7) * hb) : 0.0f;
         }
     };
-    Taker take;
-    uint4 nxa[2], nxb[2];
-    if (u_begin < u_end) load_x(R->tokens[u_begin / per_expert], 0, nxa, nxb);
+    Taker take(S);
+    uint4 nx[2][MT][2];
+    float nsc[TG];
+    if (u_begin < u_end) {
+        load_x(R->tokens[u_begin / per_expert], 0, nx);
+        load_scales(u_begin, 0, nsc);
+    }
     for (int64_t u = u_begin; u < u_end;) {
         const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
         const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
         const uint32_t mask = R->tokens[ai];
-        const int64_t e = R->expert[ai];
-        // a unit's 16 rows lie in one scale block; the pairs of a group may not
-        const float *sg[PG], *su[PG];
-#pragma unroll
-        for (int p = 0; p < PG; p++) {
-            const int row = 16 * min(r + p, per_expert - 1);
-            sg[p] = a.s_gu + ((e * 2 * I + row) >> 7) * hb;
-            su[p] = a.s_gu + ((e * 2 * I + I + row) >> 7) * hb;
-        }
         float acc[TG][MT][4] = {};
         for (int q = 0; q < ring.steps; q++) {
-            Frag<MT> f;
-            x_to_f16<MT>(nxa, xs0, f.xa);
-            if (MT == 2) x_to_f16<MT>(nxb, xs1, f.xb);
-            if (q + 1 < ring.steps)
-                load_x(mask, q + 1, nxa, nxb);
-            else if (u + n < u_end)
-                load_x(R->tokens[(u + n) / per_expert], 0, nxa, nxb);
-            const int kc = (q * ring.chunks + warp) * CH;
-            const bool active = warp < ring.chunks && kc < H;
+            Frag<MT> f[2];
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                x_to_f16<MT>(nx[c][0], xs0, f[c].xa);
+                if (MT == 2) x_to_f16<MT>(nx[c][MT - 1], xs1, f[c].xb);
+            }
             float sc[TG];
 #pragma unroll
-            for (int p = 0; p < PG; p++) {
-                sc[2 * p] = active ? __ldg(sg[p] + (kc >> 7)) : 0.0f;
-                sc[2 * p + 1] = active ? __ldg(su[p] + (kc >> 7)) : 0.0f;
+            for (int v = 0; v < TG; v++) sc[v] = nsc[v];
+            // the next step's, one step ahead
+            if (q + 1 < ring.steps) {
+                load_x(mask, q + 1, nx);
+                load_scales(u, q + 1, nsc);
+            } else if (u + n < u_end) {
+                load_x(R->tokens[(u + n) / per_expert], 0, nx);
+                load_scales(u + n, 0, nsc);
             }
+            const bool active = warp < ring.blocks && q * ring.blocks + warp < hb;
 #pragma unroll
-            for (int v = 0; v < TG; v++) {
-                if (v >= 2 * n) break;
-                if (!take.take<MT>(S, ring_at, slot_bytes, ring.slots, active, warp, lane, f)) continue;
-                float d[MT][4] = {};
-                chunk_mma<MT>(d, f);
+            for (int p = 0; p < PG; p++) {
+                if (p >= n) break;
+                slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, acc[2 * p], acc[2 * p + 1],
+                             [&](float(&o)[MT][4], const float(&d)[MT][4], int v) {
 #pragma unroll
-                for (int i = 0; i < MT; i++)
+                                 for (int i = 0; i < MT; i++)
 #pragma unroll
-                    for (int c = 0; c < 4; c++) acc[v][i][c] = __fmaf_rn(d[i][c], sc[v], acc[v][i][c]);
+                                     for (int c = 0; c < 4; c++)
+                                         o[i][c] = __fmaf_rn(d[i][c], sc[2 * p + v], o[i][c]);
+                             });
             }
         }
         reduce_warps<TG, MT>(acc, red, sums, warp, lane, 2 * n * MT * 128);
@@ -466,22 +543,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         u += n;
     }
-    if (!take.ok && lane == 0) S->abort = 1;
 }
 
 // -------------------------------------------------------------------- down --
 //   tmW  [experts * hidden] rows x inter, as (64 B, rows, inter / 64), box
-//        (64, 16, ring.chunks)
+//        (64, 16, 2 ring.blocks)
 template <int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_down(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
     constexpr int TG = 2;  // 16-row tiles sharing one pass over act
     constexpr int OUTS = TG * MT * 128;
+    static_assert(OUTS <= kPart, "workspace sums");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int slot_bytes = ring.chunks * 16 * CH;
+    const int slot_bytes = 2 * ring.blocks * 16 * SB;
     float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
-    float *sums = red + kConsumers * kSums;
+    float *sums = red + kRed;
     float *coef = sums + kSums;  // [active][tokens]: routing weight x the undone power of two
     Route *R = reinterpret_cast<Route *>(coef + kMaxActive * kMoeMaxTokens);
     Bars *S = reinterpret_cast<Bars *>(R + 1);
@@ -491,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int H = a.hidden, I = a.inter, T = a.tokens;
     init_bars(S, ring.slots);
     __syncthreads();
-    route(a, R);  // the logits were there before the previous kernel started
+    route(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
 
     // this CTA's share of the (32-row tile, expert, K step) sequence
     const int64_t steps = (int64_t)R->active * ring.steps;  // of one tile
@@ -510,8 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ai = (int)(st / ring.steps), q = (int)(st - (int64_t)ai * ring.steps);
             for (int64_t u = u_begin; u < u_end && ok; u++) {
                 const int row = (int)R->expert[ai] * H + 32 * tile;
-                for (int v = 0; v < TG && ok; v++)
-                    ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 16 * v, q * ring.chunks);
+                ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row, row + 16, q * ring.blocks * 2);
                 if (++q == ring.steps) {
                     q = 0;
                     if (++ai == R->active) {
@@ -590,31 +666,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
     };
-    auto load_step = [&](int ai, int tile, int q, Next &n0, Next &n1, float &sc) {
-        const int kc = (q * ring.chunks + warp) * CH;
-        const bool in = warp < ring.chunks && kc < I;
-        load_act(ai, g, kc + 16 * t, in, n0);
-        if (MT == 2) load_act(ai, g + 8, kc + 16 * t, in, n1);
+    auto load_step = [&](int ai, int tile, int q, Next(&n)[2][MT], float &sc) {
+        const int kb = q * ring.blocks + warp;
+        const bool in = warp < ring.blocks && kb < ib;
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int i = 0; i < MT; i++) load_act(ai, g + 8 * i, kb * SB + CH * c + 16 * t, in, n[c][i]);
         // the tile's 32 rows lie in one scale block
-        sc = in ? __ldg(a.s_d + ((int64_t)R->expert[ai] * hb + (tile >> 2)) * ib + (kc >> 7)) : 0.0f;
+        sc = in ? __ldg(a.s_d + ((int64_t)R->expert[ai] * hb + (tile >> 2)) * ib + kb) : 0.0f;
     };
 
-    Taker take;
+    Taker take(S);
     int tile = (int)(u_begin / steps);
     int64_t st = u_begin - tile * steps;
     int ai = (int)(st / ring.steps), q = (int)(st - (int64_t)ai * ring.steps);
-    Next n0, n1;
+    Next nx[2][MT];
     float sc_next = 0.0f;
-    if (u_begin < u_end) load_step(ai, tile, q, n0, n1, sc_next);
+    if (u_begin < u_end) load_step(ai, tile, q, nx, sc_next);
     for (int64_t u = u_begin; u < u_end;) {
         const int64_t first = st;
         const int64_t count = min(steps - st, u_end - u);
         float acc[TG][MT][4] = {};
         for (int64_t k = 0; k < count; k++) {
-            Frag<MT> f;
+            Frag<MT> f[2];
             const int8_t *sh = shift + ai * kMoeMaxTokens;
-            to_row(n0, sh[g], f.xa);
-            if (MT == 2) to_row(n1, sh[g + 8], f.xb);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                to_row(nx[c][0], sh[g], f[c].xa);
+                if (MT == 2) to_row(nx[c][MT - 1], sh[g + 8], f[c].xb);
+            }
             const float sc = sc_next;
             float cf[MT][2];
 #pragma unroll
@@ -624,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int m = 8 * i + 2 * t + c;
                     cf[i][c] = ((R->tokens[ai] >> m) & 1) ? coef[ai * kMoeMaxTokens + m] * sc : 0.0f;
                 }
-            const bool active = warp < ring.chunks && (q * ring.chunks + warp) * CH < I;
+            const bool active = warp < ring.blocks && q * ring.blocks + warp < ib;
             int tile1 = tile;
             if (++q == ring.steps) {
                 q = 0;
@@ -633,17 +714,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tile1++;
                 }
             }
-            if (u + k + 1 < u_end) load_step(ai, tile1, q, n0, n1, sc_next);
+            if (u + k + 1 < u_end) load_step(ai, tile1, q, nx, sc_next);
+            slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, acc[0], acc[1],
+                         [&](float(&o)[MT][4], const float(&d)[MT][4], int) {
 #pragma unroll
-            for (int v = 0; v < TG; v++) {
-                if (!take.take<MT>(S, ring_at, slot_bytes, ring.slots, active, warp, lane, f)) continue;
-                float d[MT][4] = {};
-                chunk_mma<MT>(d, f);
+                             for (int i = 0; i < MT; i++)
 #pragma unroll
-                for (int i = 0; i < MT; i++)
-#pragma unroll
-                    for (int c = 0; c < 4; c++) acc[v][i][c] = __fmaf_rn(d[i][c], cf[i][c & 1], acc[v][i][c]);
-            }
+                                 for (int c = 0; c < 4; c++) o[i][c] = __fmaf_rn(d[i][c], cf[i][c & 1], o[i][c]);
+                         });
         }
         reduce_warps<TG, MT>(acc, red, sums, warp, lane, OUTS);
         u += count;
@@ -655,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t t0 = (int64_t)tile * steps;
             b0 = (int)(((t0 + 1) * shares - 1) / all);
             b1 = (int)(((t0 + steps) * shares - 1) / all);
-            float *mine = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kSums;
+            float *mine = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kPart;
             for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) __stcg(mine + v, sums[v]);
             __threadfence();
             consumers_sync();
@@ -673,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a share's slot: 1 where it starts at the tile's first step
                         const int64_t begin = all * b / shares;
                         const int head = begin <= (int64_t)tile * steps;
-                        sum += __ldcg(ws.part + ((int64_t)b * 2 + head) * kSums + v);
+                        sum += __ldcg(ws.part + ((int64_t)b * 2 + head) * kPart + v);
                     }
                 }
                 const int w = v / (MT * 128), i = (v >> 7) % MT, r = (v >> 5) & 3, ln = v & 31;
@@ -686,24 +764,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             tile++;
         }
     }
-    if (!take.ok && lane == 0) S->abort = 1;
 }
 
 // -------------------------------------------------------------------- host --
 
 constexpr size_t kSmemMax = 232448;
-constexpr size_t gate_up_fixed() { return 1024 + (kConsumers + 1) * kSums * 4 + sizeof(Route) + sizeof(Bars); }
+constexpr size_t gate_up_fixed() { return 1024 + (kRed + kSums) * 4 + sizeof(Route) + sizeof(Bars); }
 constexpr size_t down_fixed() {
     return gate_up_fixed() + (size_t)kMaxActive * kMoeMaxTokens * (sizeof(float) + 1);
 }
 
-// Boxes of equal size, at most 1 KB of K, and as many as fit.
+// Boxes of equal size, at most 1 KB of K, and as many slots as fit.
 Ring ring_for(int k, size_t fixed) {
     Ring r;
-    const int chunks = k / CH;
-    r.steps = (chunks + 15) / 16;
-    r.chunks = (chunks + r.steps - 1) / r.steps;
-    const int room = (int)((kSmemMax - fixed) / ((size_t)r.chunks * 16 * CH));
+    const int blocks = k / SB;
+    r.steps = (blocks + kConsumers - 1) / kConsumers;
+    r.blocks = (blocks + r.steps - 1) / r.steps;
+    const int room = (int)((kSmemMax - fixed) / ((size_t)r.blocks * 2 * 16 * SB));
     r.slots = room < kMaxSlots ? room : kMaxSlots;
     return r;
 }
@@ -714,7 +791,7 @@ size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
     const size_t pairs = (size_t)tokens * topk;
     const size_t act = align256(pairs * inter * sizeof(__half)), ex = align256(pairs * (inter / 16)),
                  count = align256((size_t)hidden / 32 * sizeof(int)),
-                 part = (size_t)sm_count() * 2 * kSums * sizeof(float);
+                 part = (size_t)sm_count() * 2 * kPart * sizeof(float);
     if (ws) {
         uint8_t *b = static_cast<uint8_t *>(p);
         ws->act = reinterpret_cast<__half *>(b);
@@ -730,7 +807,7 @@ cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Ri
                        const Ws &ws, cudaStream_t s) {
     alignas(64) CUtensorMap tm;
     const uint64_t d[3] = {CH, (uint64_t)rows, (uint64_t)k / CH}, st[2] = {(uint64_t)k, CH};
-    const uint32_t box[3] = {CH, 16, (uint32_t)ring.chunks};
+    const uint32_t box[3] = {CH, 16, (uint32_t)(2 * ring.blocks)};
     if (!make_tmap(&tm, w, 1, 3, d, st, box, 64)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sm_count());
@@ -760,10 +837,10 @@ template <int MT> cudaError_t launch_mt(const MoeArgs &a, cudaStream_t s) {
     ws_layout(a.workspace, a.tokens, a.hidden, a.inter, a.topk, &ws);
     const Ring up = ring_for(a.hidden, gate_up_fixed()), down = ring_for(a.inter, down_fixed());
     e = launch_one(k_moe_gate_up<MT>, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, up,
-                   gate_up_fixed() + (size_t)up.slots * up.chunks * 16 * CH, a, ws, s);
+                   gate_up_fixed() + (size_t)up.slots * up.blocks * 2 * 16 * SB, a, ws, s);
     if (e != cudaSuccess) return e;
     return launch_one(k_moe_down<MT>, a.w_d, (int64_t)a.experts * a.hidden, a.inter, down,
-                      down_fixed() + (size_t)down.slots * down.chunks * 16 * CH, a, ws, s);
+                      down_fixed() + (size_t)down.slots * down.blocks * 2 * 16 * SB, a, ws, s);
 }
 
 }  // namespace
