@@ -9,9 +9,8 @@
 // warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, two
 // boxes to a slot, and eight consumer warps that split a box's K into its
 // 128-wide scale blocks (E4M3 -> FP16 exactly, FP16 MMAs with FP32 sums, each
-// block's sum times its scale).  The MMA's eight (or sixteen) columns are the tokens themselves: a
-// token that did not choose the expert has zeros there, which costs nothing
-// beside the stream, and no gather or scatter is needed.
+// block's sum times its scale).  The MMA's eight columns are tokens: those that chose the expert
+// (gate, up), or all of them with zeros where they did not (down).
 //
 //   k_moe_gate_up  every CTA routes all tokens by itself (some hundred
 //                  instructions per token), then takes an equal share of the
@@ -107,8 +106,11 @@ __device__ __forceinline__ float route_exp(float l, float mx) {
 }
 
 // Routes every token (a warp each, in turn) and lists the reached experts.
+// SPLIT: an expert with more than eight tokens is listed twice, with its first
+// eight and with the others.
 // `keys`: kMoeMaxTokens x kMoeMaxExperts words.  Called by all threads of the
 // CTA.
+template <bool SPLIT>
 __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < kMoeMaxExperts; e += kThreads) R->slot[e] = 0;
@@ -166,13 +168,14 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
     }
     __syncthreads();
     constexpr int HALVES = kMoeMaxExperts / (32 * kConsumers);
-    uint32_t mask[HALVES], ballot[HALVES];
+    uint32_t mask[HALVES], one[HALVES], two[HALVES];
     if (warp < kConsumers) {
 #pragma unroll
         for (int i = 0; i < HALVES; i++) {
             mask[i] = R->slot[i * 32 * kConsumers + threadIdx.x];
-            ballot[i] = __ballot_sync(0xFFFFFFFFu, mask[i] != 0);
-            if (lane == 0) R->warp_count[i * kConsumers + warp] = __popc(ballot[i]);
+            one[i] = __ballot_sync(0xFFFFFFFFu, mask[i] != 0);
+            two[i] = SPLIT ? __ballot_sync(0xFFFFFFFFu, __popc(mask[i]) > 8) : 0u;
+            if (lane == 0) R->warp_count[i * kConsumers + warp] = __popc(one[i]) + __popc(two[i]);
         }
     }
     __syncthreads();
@@ -180,19 +183,31 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
 #pragma unroll
         for (int i = 0; i < HALVES; i++) {
             const int w = i * kConsumers + warp, e = i * 32 * kConsumers + (int)threadIdx.x;
+            const uint32_t below = (1u << lane) - 1u;
             const int before = lane < w ? R->warp_count[lane] : 0;  // (at most 16 warps' counts)
-            const int at = (int)__reduce_add_sync(0xFFFFFFFFu, before) + __popc(ballot[i] & ((1u << lane) - 1u));
+            const int at = (int)__reduce_add_sync(0xFFFFFFFFu, before) + __popc(one[i] & below) + __popc(two[i] & below);
+            uint32_t first = mask[i];
+            if (SPLIT)
+                while (__popc(first) > 8) first &= ~(0x80000000u >> __clz(first));
             if (mask[i]) {
                 R->expert[at] = (uint16_t)e;
-                R->tokens[at] = (uint16_t)mask[i];
+                R->tokens[at] = (uint16_t)first;
+                if (first != mask[i]) {
+                    R->expert[at + 1] = (uint16_t)e;
+                    R->tokens[at + 1] = (uint16_t)(mask[i] & ~first);
+                }
                 R->slot[e] = at;
             }
-            if (e == kMoeMaxExperts - 1) R->active = at + (mask[i] != 0);
+            if (e == kMoeMaxExperts - 1) R->active = at + (mask[i] != 0) + (first != mask[i]);
         }
     }
     __syncthreads();
     const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
-    if (t < a.tokens && j < a.topk && R->weight[t][j] > 0.0f) R->pick[R->slot[R->id[t][j]]][t] = (uint8_t)j;
+    if (t < a.tokens && j < a.topk && R->weight[t][j] > 0.0f) {
+        int at = R->slot[R->id[t][j]];
+        if (SPLIT) at += !((R->tokens[at] >> t) & 1);
+        R->pick[at][t] = (uint8_t)j;
+    }
     __syncthreads();
 }
 static_assert(kMoeMaxExperts % (32 * kConsumers) == 0 && kMoeMaxExperts / 32 <= 32 && kMoeMaxTopk == 16 &&
@@ -241,13 +256,28 @@ struct Taker {
     }
 };
 
+// d (+)= 16 rows x 64 of K times eight tokens; a_w, b_w the E4M3 bytes of rows
+// g and g + 8, x the FP16 activations.
+__device__ __forceinline__ void chunk_mma_8(float (&d)[4], const uint4 &wa, const uint4 &wb, const uint32_t (&x)[8]) {
+    const uint32_t a_w[4] = {wa.x, wa.y, wa.z, wa.w};
+    const uint32_t b_w[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        uint32_t a[4];
+        e4m3x4_to_f16x2(a_w[j], a[0], a[2]);
+        e4m3x4_to_f16x2(b_w[j], a[1], a[3]);
+        mma_f16_16816(d, a, x[2 * j], x[2 * j + 1]);
+    }
+}
+
 // The next slot: this warp's scale block (two chunks) of each of its two boxes
-// times the activation fragments f[0], f[1], as two independent chains of
-// MMAs, handed to `add` with its accumulator.
+// times the activation fragments x[chunk][token half], as independent chains
+// of MMAs, handed to `add` with its accumulator.  tokens: a half without any
+// is skipped.
 template <int MT, class Add>
 __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, int slot_bytes, int slots, bool active,
-                                         int warp, int lane, Frag<MT> (&f)[2], float (&acc0)[MT][4],
-                                         float (&acc1)[MT][4], Add &&add) {
+                                         int warp, int lane, uint32_t tokens, const uint32_t (&x)[2][MT][8],
+                                         float (&acc0)[MT][4], float (&acc1)[MT][4], Add &&add) {
     const uint32_t at = take.take(S, ring, slot_bytes) + warp * 2 * 16 * CH;
     const int g = lane >> 2, t = lane & 3;
     uint4 w[2][2][2];  // [box][chunk][row g, g + 8]
@@ -263,17 +293,20 @@ __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, in
     }
     take.give_back(slots, lane);
     if (!active) return;
-    float d[2][MT][4] = {};
 #pragma unroll
-    for (int c = 0; c < 2; c++)
+    for (int i = 0; i < MT; i++) {
+        if (MT == 2 && ((tokens >> (8 * i)) & 0xFFu) == 0) continue;
+        float d[2][2][4] = {};  // [box][chunk]
 #pragma unroll
-        for (int v = 0; v < 2; v++) {
-            f[c].wa = w[v][c][0];
-            f[c].wb = w[v][c][1];
-            chunk_mma<MT>(d[v], f[c]);
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int v = 0; v < 2; v++) chunk_mma_8(d[v][c], w[v][c][0], w[v][c][1], x[c][i]);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            add(acc0[i][k], d[0][0][k] + d[0][1][k], 0, i, k);
+            add(acc1[i][k], d[1][0][k] + d[1][1][k], 1, i, k);
         }
-    add(acc0, d[0], 0);
-    add(acc1, d[1], 1);
+    }
 }
 
 // Producer side, one thread.
@@ -352,10 +385,9 @@ __device__ __forceinline__ int exp_shift(int e) { return e == 0 ? 127 : min(14 -
 // ---------------------------------------------------------------- gate, up --
 //   tmW  [experts * 2 inter] rows x hidden, as (64 B, rows, hidden / 64), box
 //        (64, 16, 2 ring.blocks)
-template <int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_gate_up(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
-    constexpr int PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
+    constexpr int MT = 1, PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int slot_bytes = 2 * ring.blocks * 16 * SB;
@@ -373,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one writes before it has completed, and everything before this one has
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    route(a, R, reinterpret_cast<uint32_t *>(red));
+    route<true>(a, R, reinterpret_cast<uint32_t *>(red));
 
     // this CTA's share of the (expert, 16 rows) units
     const int per_expert = I >> 4;
@@ -438,22 +470,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7;
-    const float xs0 = pow2i(row_shift(S->rowmax[g])), xs1 = MT == 2 ? pow2i(row_shift(S->rowmax[g + 8])) : 0.0f;
-    const uint16_t *x0 = a.x + (int64_t)min(g, T - 1) * H + SB * warp + 16 * t;
-    const uint16_t *x1 = a.x + (int64_t)min(g + 8, T - 1) * H + SB * warp + 16 * t;
-    // this lane's activations of step q, [chunk][token half][16-byte half]:
-    // zeros for a token that did not choose the expert, and past the end of K
-    auto load_x = [&](uint32_t mask, int q, uint4(&x)[2][MT][2]) {
-        const int k = q * ring.blocks * SB;
-        const bool in = warp < ring.blocks && k + SB * warp < H;
+    // The MMA's columns are the listed expert's tokens, compactly: column c is
+    // its c-th token (-1 past the last).
+    auto column = [&](uint32_t mask, int c) {
+        for (int i = 0; i < c; i++) mask &= mask - 1;
+        return __ffs(mask) - 1;
+    };
+    // this lane's activations of step q for token m, [chunk][16-byte half]:
+    // zeros without a token and past the end of K
+    auto load_x = [&](int m, int q, uint4(&x)[2][2]) {
+        const int k = (q * ring.blocks + warp) * SB;
+        const bool in = m >= 0 && warp < ring.blocks && k < H;
+        const uint16_t *p = a.x + (int64_t)max(m, 0) * H + k + 16 * t;
 #pragma unroll
         for (int c = 0; c < 2; c++)
 #pragma unroll
-            for (int i = 0; i < MT; i++)
-#pragma unroll
-                for (int h = 0; h < 2; h++)
-                    x[c][i][h] = in && ((mask >> (g + 8 * i)) & 1) ? ldg_nc_v4((i ? x1 : x0) + k + CH * c + 8 * h)
-                                                                   : make_uint4(0u, 0u, 0u, 0u);
+            for (int h = 0; h < 2; h++) x[c][h] = in ? ldg_nc_v4(p + CH * c + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
     };
     // the scales of this warp's block of step q for the tiles of the group at
     // unit u (a unit's 16 rows lie in one scale block; a group's may not)
@@ -470,57 +502,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
     Taker take(S);
-    uint4 nx[2][MT][2];
+    uint4 nx[2][2];
     float nsc[TG];
+    int m_next = -1;
     if (u_begin < u_end) {
-        load_x(R->tokens[u_begin / per_expert], 0, nx);
+        m_next = column(R->tokens[u_begin / per_expert], g);
+        load_x(m_next, 0, nx);
         load_scales(u_begin, 0, nsc);
     }
     for (int64_t u = u_begin; u < u_end;) {
         const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
         const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
         const uint32_t mask = R->tokens[ai];
+        const int my = m_next;  // this lane's token
+        const float xs = pow2i(row_shift(S->rowmax[max(my, 0)]));
         float acc[TG][MT][4] = {};
         for (int q = 0; q < ring.steps; q++) {
-            Frag<MT> f[2];
+            uint32_t f[2][MT][8];
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                x_to_f16<MT>(nx[c][0], xs0, f[c].xa);
-                if (MT == 2) x_to_f16<MT>(nx[c][MT - 1], xs1, f[c].xb);
-            }
+            for (int c = 0; c < 2; c++) x_to_f16<MT>(nx[c], xs, f[c][0]);
             float sc[TG];
 #pragma unroll
             for (int v = 0; v < TG; v++) sc[v] = nsc[v];
             // the next step's, one step ahead
             if (q + 1 < ring.steps) {
-                load_x(mask, q + 1, nx);
+                load_x(my, q + 1, nx);
                 load_scales(u, q + 1, nsc);
             } else if (u + n < u_end) {
-                load_x(R->tokens[(u + n) / per_expert], 0, nx);
+                m_next = column(R->tokens[(u + n) / per_expert], g);
+                load_x(m_next, 0, nx);
                 load_scales(u + n, 0, nsc);
             }
             const bool active = warp < ring.blocks && q * ring.blocks + warp < hb;
 #pragma unroll
             for (int p = 0; p < PG; p++) {
                 if (p >= n) break;
-                slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, acc[2 * p], acc[2 * p + 1],
-                             [&](float(&o)[MT][4], const float(&d)[MT][4], int v) {
-#pragma unroll
-                                 for (int i = 0; i < MT; i++)
-#pragma unroll
-                                     for (int c = 0; c < 4; c++)
-                                         o[i][c] = __fmaf_rn(d[i][c], sc[2 * p + v], o[i][c]);
-                             });
+                slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, mask, f, acc[2 * p],
+                             acc[2 * p + 1],
+                             [&](float &o, float d, int v, int, int) { o = __fmaf_rn(d, sc[2 * p + v], o); });
             }
         }
         reduce_warps<TG, MT>(acc, red, sums, warp, lane, 2 * n * MT * 128);
-        // silu(gate) * up: a warp takes one (pair, token half, column parity),
-        // a lane rows g and g + 8 of token 8 i + 2 t + parity
-        if (warp < n * MT * 2) {
-            const int p = warp / (2 * MT), i = (warp >> 1) % MT, c = warp & 1;
-            const int m = 8 * i + 2 * t + c;
-            const float unscale = pow2i(-row_shift(S->rowmax[m]));
-            const float *gs = sums + ((2 * p * MT + i) * 4 + c) * 32 + lane, *us = gs + MT * 128;
+        // silu(gate) * up: a warp takes one (pair, column parity), a lane rows
+        // g and g + 8 of column 2 t + parity
+        if (warp < 2 * n) {
+            const int p = warp >> 1, c = warp & 1;
+            const int m = column(mask, 2 * t + c);
+            const float unscale = pow2i(-row_shift(S->rowmax[max(m, 0)]));
+            const float *gs = sums + (2 * p * 4 + c) * 32 + lane, *us = gs + 128;
             float v[2];
 #pragma unroll
             for (int k = 0; k < 2; k++) {
@@ -531,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            if ((mask >> m) & 1) {
+            if (m >= 0) {
                 const int64_t pair = (int64_t)m * a.topk + R->pick[ai][m];
                 const int ex = (int)(__float_as_uint(mx) >> 23);
                 const float s = pow2i(exp_shift(ex));
@@ -568,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int H = a.hidden, I = a.inter, T = a.tokens;
     init_bars(S, ring.slots);
     __syncthreads();
-    route(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
+    route<false>(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
 
     // this CTA's share of the (32-row tile, expert, K step) sequence
     const int64_t steps = (int64_t)R->active * ring.steps;  // of one tile
@@ -689,13 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t count = min(steps - st, u_end - u);
         float acc[TG][MT][4] = {};
         for (int64_t k = 0; k < count; k++) {
-            Frag<MT> f[2];
+            uint32_t f[2][MT][8];
+            const uint32_t mask = R->tokens[ai];
             const int8_t *sh = shift + ai * kMoeMaxTokens;
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                to_row(nx[c][0], sh[g], f[c].xa);
-                if (MT == 2) to_row(nx[c][MT - 1], sh[g + 8], f[c].xb);
-            }
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int i = 0; i < MT; i++) to_row(nx[c][i], sh[g + 8 * i], f[c][i]);
             const float sc = sc_next;
             float cf[MT][2];
 #pragma unroll
@@ -703,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
                     const int m = 8 * i + 2 * t + c;
-                    cf[i][c] = ((R->tokens[ai] >> m) & 1) ? coef[ai * kMoeMaxTokens + m] * sc : 0.0f;
+                    cf[i][c] = ((mask >> m) & 1) ? coef[ai * kMoeMaxTokens + m] * sc : 0.0f;
                 }
             const bool active = warp < ring.blocks && q * ring.blocks + warp < ib;
             int tile1 = tile;
@@ -715,13 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (u + k + 1 < u_end) load_step(ai, tile1, q, nx, sc_next);
-            slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, acc[0], acc[1],
-                         [&](float(&o)[MT][4], const float(&d)[MT][4], int) {
-#pragma unroll
-                             for (int i = 0; i < MT; i++)
-#pragma unroll
-                                 for (int c = 0; c < 4; c++) o[i][c] = __fmaf_rn(d[i][c], cf[i][c & 1], o[i][c]);
-                         });
+            slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, mask, f, acc[0], acc[1],
+                         [&](float &o, float d, int, int i, int r) { o = __fmaf_rn(d, cf[i][r & 1], o); });
         }
         reduce_warps<TG, MT>(acc, red, sums, warp, lane, OUTS);
         u += count;
@@ -827,7 +851,7 @@ cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Ri
 template <int MT> cudaError_t launch_mt(const MoeArgs &a, cudaStream_t s) {
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        const cudaError_t err = cudaFuncSetAttribute(k_moe_gate_up<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t err = cudaFuncSetAttribute(k_moe_gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      (int)kSmemMax);
         if (err != cudaSuccess) return err;
         return cudaFuncSetAttribute(k_moe_down<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
@@ -836,7 +860,7 @@ template <int MT> cudaError_t launch_mt(const MoeArgs &a, cudaStream_t s) {
     Ws ws;
     ws_layout(a.workspace, a.tokens, a.hidden, a.inter, a.topk, &ws);
     const Ring up = ring_for(a.hidden, gate_up_fixed()), down = ring_for(a.inter, down_fixed());
-    e = launch_one(k_moe_gate_up<MT>, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, up,
+    e = launch_one(k_moe_gate_up, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, up,
                    gate_up_fixed() + (size_t)up.slots * up.blocks * 2 * 16 * SB, a, ws, s);
     if (e != cudaSuccess) return e;
     return launch_one(k_moe_down<MT>, a.w_d, (int64_t)a.experts * a.hidden, a.inter, down,

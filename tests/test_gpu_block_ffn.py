@@ -338,7 +338,7 @@ class Moe:
     (1, 128, 128, 1, 1, 1), (1, 2048, 768, 16, 8, 1), (2, 1024, 384, 8, 2, 0), (3, 640, 128, 5, 5, 0),
     (7, 256, 256, 9, 3, 1), (8, 1408, 640, 12, 4, 0), (9, 512, 128, 33, 2, 1), (16, 1024, 1408, 24, 8, 0),
     (16, 256, 128, 4, 1, 1), (16, 384, 256, 300, 16, 0), (5, 128, 2176, 6, 2, 1), (13, 5120, 128, 8, 3, 0),
-    (4, 7168, 256, 3, 2, 1)])
+    (4, 7168, 256, 3, 2, 1), (16, 512, 256, 3, 2, 1), (16, 256, 640, 1, 1, 0), (12, 384, 1408, 2, 2, 0)])
 def test_moe(t, h, i, e, topk, renorm):
     m = Moe(t, h, i, e, topk, renorm, seed=t)
     m()
