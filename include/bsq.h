@@ -477,9 +477,8 @@ BSQ_API bsq_status fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, 
  * Errors: tokens outside 0..16, experts <= 0, topk outside 1..experts,
  * hidden or inter not a positive multiple of 16, renormalise not 0 or 1,
  * ws_bytes too small -> INVALID_ARG; hidden or inter not a multiple of 128,
- * topk > 16, experts > 512, experts * 2*inter or experts * hidden above
- * 2^31 - 1 -> UNSUPPORTED.  x, weights, out, workspace 16-byte aligned, the
- * rest 4-byte.
+ * or above 65536, topk > 16, experts > 512 -> UNSUPPORTED.  x, weights, out,
+ * workspace 16-byte aligned, the rest 4-byte.
  * ---------------------------------------------------------------------- */
 BSQ_API bsq_status fp8_moe_blockscaled(const uint16_t *x, const float *logits, const uint8_t *w_gate_up,
                                const float *gate_up_scale, const uint8_t *w_down,

@@ -3,9 +3,7 @@
 // that fails it launches nothing and needs no GPU.
 #include <atomic>
 #include <cfloat>
-#include <climits>
 #include <cmath>
-#include <cstdint>
 
 #include "../../include/bsq.h"
 #include "bsq_internal.h"
@@ -295,7 +293,9 @@ namespace {
 bsq_status check_moe_shape(int tokens, int hidden, int inter, int topk) {
     if (tokens < 0 || tokens > bsq::kMoeMaxTokens || hidden <= 0 || inter <= 0 || hidden % 16 || inter % 16 || topk < 1)
         return BSQ_ERR_INVALID_ARG;
-    if (hidden % 128 || inter % 128 || topk > bsq::kMoeMaxTopk) return BSQ_ERR_UNSUPPORTED;
+    if (hidden % 128 || inter % 128 || hidden > bsq::kMoeMaxWidth || inter > bsq::kMoeMaxWidth ||
+        topk > bsq::kMoeMaxTopk)
+        return BSQ_ERR_UNSUPPORTED;
     return BSQ_OK;
 }
 
@@ -314,10 +314,7 @@ bsq_status fp8_moe_blockscaled(const uint16_t *x, const float *logits, const uin
     if (experts <= 0 || topk > experts || (renormalise != 0 && renormalise != 1)) return BSQ_ERR_INVALID_ARG;
     bsq_status st = check_moe_shape(tokens, hidden, inter, topk);
     if (st != BSQ_OK) return st;
-    // the copies address weight rows and K columns with 32-bit coordinates
-    if (experts > bsq::kMoeMaxExperts || (int64_t)experts * 2 * inter > INT32_MAX ||
-        (int64_t)experts * hidden > INT32_MAX)
-        return BSQ_ERR_UNSUPPORTED;
+    if (experts > bsq::kMoeMaxExperts) return BSQ_ERR_UNSUPPORTED;
     if (tokens == 0) return BSQ_OK;
     if (!x || !logits || !w_gate_up || !gate_up_scale || !w_down || !down_scale || !out || !workspace)
         return BSQ_ERR_INVALID_ARG;

@@ -97,7 +97,8 @@ cudaError_t launch_fp8_gemm_blockscaled_small(const uint8_t *a, const float *a_s
                                               cudaStream_t s);
 
 // ---- launchers (moe_fp8.cu) ----
-constexpr int kMoeMaxTokens = 16, kMoeMaxTopk = 16, kMoeMaxExperts = 512;
+// (with these widths every count of rows or steps fits 32 bits)
+constexpr int kMoeMaxTokens = 16, kMoeMaxTopk = 16, kMoeMaxExperts = 512, kMoeMaxWidth = 65536;
 struct MoeArgs {
     const uint16_t *x;       // [tokens, hidden] BF16
     const float *logits;     // [tokens, experts]

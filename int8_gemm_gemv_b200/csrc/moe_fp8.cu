@@ -129,20 +129,16 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
             }
         }
         const float mx = key_logit(__reduce_max_sync(0xFFFFFFFFu, best));
-        float sum = 0.0f, mine = 0.0f;
-        int my_id = 0;
-        if (!a.renormalise) {
+        float sum = 0.0f;
+        if (!a.renormalise)
             for (int e = lane; e < a.experts; e += 32) sum += route_exp(key_logit(key[e]), mx);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        }
+        uint32_t my_key = 0;  // lane j: the j-th choice
+        int my_id = 0;
         for (int j = 0; j < a.topk; j++) {
             const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
             const int e = __reduce_min_sync(0xFFFFFFFFu, best == top ? at : kMoeMaxExperts);
-            const float p = route_exp(key_logit(top), mx);
-            if (a.renormalise) sum += p;
             if (lane == j) {
-                mine = p;
+                my_key = top;
                 my_id = e;
             }
             if ((e & 31) == lane) {  // its owner looks for its next
@@ -156,8 +152,11 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
                     }
                 }
             }
-            __syncwarp();
         }
+        const float mine = lane < a.topk ? route_exp(key_logit(my_key), mx) : 0.0f;
+        if (a.renormalise) sum = mine;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane < a.topk) {
             const float w = sum > 0.0f ? __fdiv_rn(mine, sum) : 0.0f;
             R->id[t][lane] = (uint16_t)my_id;
@@ -370,6 +369,21 @@ __device__ __forceinline__ void reduce_warps(const float (&acc)[TG][MT][4], floa
     consumers_sync();
 }
 
+// Share b of g of `all` steps: equal to within one, none empty while b < all.
+struct Share {
+    int begin, end;
+};
+__device__ __forceinline__ Share share_of(int all, int b, int g) {
+    const int per = all / g, more = all - per * g;
+    const int begin = b * per + min(b, more);
+    return {begin, begin + per + (b < more)};
+}
+// The share that step u lies in.
+__device__ __forceinline__ int share_at(int all, int u, int g) {
+    const int per = all / g, more = all - per * g;
+    return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
+}
+
 // Workspace layout.
 struct Ws {
     __half *act;       // [tokens * topk, inter], times a power of two per 16
@@ -409,17 +423,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // this CTA's share of the (expert, 16 rows) units
     const int per_expert = I >> 4;
-    const int64_t units = (int64_t)R->active * per_expert;
-    const int64_t u_begin = units * blockIdx.x / gridDim.x, u_end = units * (blockIdx.x + 1) / gridDim.x;
+    const Share mine = share_of(R->active * per_expert, blockIdx.x, gridDim.x);
+    const int u_begin = mine.begin, u_end = mine.end;
 
     if (warp == kConsumers) {
         if (elect_one()) {
             prefetch_tensormap(&tmW);
             Giver give;
             bool ok = true;
-            for (int64_t u = u_begin; u < u_end && ok;) {
-                const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
-                const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
+            for (int u = u_begin; u < u_end && ok;) {
+                const int ai = u / per_expert, r = u - ai * per_expert;
+                const int n = min(min(PG, per_expert - r), u_end - u);
                 const int row = (int)R->expert[ai] * 2 * I + 16 * r;
                 for (int q = 0; q < ring.steps && ok; q++)
                     for (int p = 0; p < n && ok; p++)
@@ -432,6 +446,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring_at = smem_u32(base);
+    const int hb = H >> 7;
+    // The MMA's columns are the listed expert's tokens, compactly: column c is
+    // its c-th token (-1 past the last).
+    auto column = [&](uint32_t mask, int c) {
+        for (int i = 0; i < c; i++) mask &= mask - 1;
+        return __ffs(mask) - 1;
+    };
+    // this lane's activations of step q for token m, [chunk][16-byte half]:
+    // zeros without a token and past the end of K
+    auto load_x = [&](int m, int q, uint4(&x)[2][2]) {
+        const int k = (q * ring.blocks + warp) * SB;
+        const bool in = m >= 0 && warp < ring.blocks && k < H;
+        const uint16_t *p = a.x + (int64_t)max(m, 0) * H + k + 16 * t;
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) x[c][h] = in ? ldg_nc_v4(p + CH * c + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    // the scales of this warp's block of step q for the group that starts at row
+    // unit r of the listed expert ai (a unit's 16 rows lie in one scale block;
+    // a group's may not)
+    auto load_scales = [&](int ai, int r, int q, float(&sc)[TG]) {
+        const int kb = q * ring.blocks + warp;
+        const bool in = warp < ring.blocks && kb < hb;
+#pragma unroll
+        for (int p = 0; p < PG; p++) {
+            const int64_t row = (int64_t)R->expert[ai] * 2 * I + 16 * min(r + p, per_expert - 1);
+            const float *s = a.s_gu + (row >> 7) * hb + kb;
+            sc[2 * p] = in ? __ldg(s) : 0.0f;
+            sc[2 * p + 1] = in ? __ldg(s + (int64_t)(I >> 7) * hb) : 0.0f;
+        }
+    };
+    Taker take(S);
+    uint4 nx[2][2];
+    float nsc[TG];
+    int m_next = -1, ai = u_begin / per_expert, r = u_begin - ai * per_expert;
+    if (u_begin < u_end) {
+        m_next = column(R->tokens[ai], g);
+        load_x(m_next, 0, nx);
+        load_scales(ai, r, 0, nsc);
+    }
     // each token's largest magnitude, found by all consumer warps together (the
     // first weight copies are on their way)
     {
@@ -465,54 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = threadIdx.x; i < (H >> 5); i += 32 * kConsumers) ws.count[i] = 0;
     }
-    consumers_sync();
 
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t ring_at = smem_u32(base);
-    const int hb = H >> 7;
-    // The MMA's columns are the listed expert's tokens, compactly: column c is
-    // its c-th token (-1 past the last).
-    auto column = [&](uint32_t mask, int c) {
-        for (int i = 0; i < c; i++) mask &= mask - 1;
-        return __ffs(mask) - 1;
-    };
-    // this lane's activations of step q for token m, [chunk][16-byte half]:
-    // zeros without a token and past the end of K
-    auto load_x = [&](int m, int q, uint4(&x)[2][2]) {
-        const int k = (q * ring.blocks + warp) * SB;
-        const bool in = m >= 0 && warp < ring.blocks && k < H;
-        const uint16_t *p = a.x + (int64_t)max(m, 0) * H + k + 16 * t;
-#pragma unroll
-        for (int c = 0; c < 2; c++)
-#pragma unroll
-            for (int h = 0; h < 2; h++) x[c][h] = in ? ldg_nc_v4(p + CH * c + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    // the scales of this warp's block of step q for the tiles of the group at
-    // unit u (a unit's 16 rows lie in one scale block; a group's may not)
-    auto load_scales = [&](int64_t u, int q, float(&sc)[TG]) {
-        const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
-        const int kb = q * ring.blocks + warp;
-        const bool in = warp < ring.blocks && kb < hb;
-#pragma unroll
-        for (int p = 0; p < PG; p++) {
-            const int64_t row = (int64_t)R->expert[ai] * 2 * I + 16 * min(r + p, per_expert - 1);
-            const float *s = a.s_gu + (row >> 7) * hb + kb;
-            sc[2 * p] = in ? __ldg(s) : 0.0f;
-            sc[2 * p + 1] = in ? __ldg(s + (int64_t)(I >> 7) * hb) : 0.0f;
-        }
-    };
-    Taker take(S);
-    uint4 nx[2][2];
-    float nsc[TG];
-    int m_next = -1;
-    if (u_begin < u_end) {
-        m_next = column(R->tokens[u_begin / per_expert], g);
-        load_x(m_next, 0, nx);
-        load_scales(u_begin, 0, nsc);
-    }
-    for (int64_t u = u_begin; u < u_end;) {
-        const int ai = (int)(u / per_expert), r = (int)(u - (int64_t)ai * per_expert);
-        const int n = (int)min((int64_t)min(PG, per_expert - r), u_end - u);
+    consumers_sync();
+    for (int u = u_begin; u < u_end;) {
+        const int n = min(min(PG, per_expert - r), u_end - u);
+        const int ai1 = r + n == per_expert ? ai + 1 : ai, r1 = r + n == per_expert ? 0 : r + n;  // the next group
         const uint32_t mask = R->tokens[ai];
         const int my = m_next;  // this lane's token
         const float xs = pow2i(row_shift(S->rowmax[max(my, 0)]));
@@ -527,11 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the next step's, one step ahead
             if (q + 1 < ring.steps) {
                 load_x(my, q + 1, nx);
-                load_scales(u, q + 1, nsc);
+                load_scales(ai, r, q + 1, nsc);
             } else if (u + n < u_end) {
-                m_next = column(R->tokens[(u + n) / per_expert], g);
+                m_next = column(R->tokens[ai1], g);
                 load_x(m_next, 0, nx);
-                load_scales(u + n, 0, nsc);
+                load_scales(ai1, r1, 0, nsc);
             }
             const bool active = warp < ring.blocks && q * ring.blocks + warp < hb;
 #pragma unroll
@@ -571,6 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         u += n;
+        ai = ai1;
+        r = r1;
     }
 }
 
@@ -599,22 +615,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     route<false>(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
 
-    // this CTA's share of the (32-row tile, expert, K step) sequence
-    const int64_t steps = (int64_t)R->active * ring.steps;  // of one tile
-    const int64_t all = steps * (H >> 5);
-    // no share is empty: the count of a shared tile's shares relies on it
-    const int64_t shares = min((int64_t)gridDim.x, max(all, (int64_t)1));
-    const int64_t u_begin = min(all, all * blockIdx.x / shares), u_end = min(all, all * (blockIdx.x + 1) / shares);
+    // this CTA's share of the (32-row tile, expert, K step) sequence; no share
+    // is empty, which the count of a shared tile's shares relies on
+    const int steps = R->active * ring.steps, all = steps * (H >> 5);  // of one tile, of all
+    const int shares = max(min((int)gridDim.x, all), 1);
+    const Share mine = (int)blockIdx.x < shares ? share_of(all, blockIdx.x, shares) : Share{all, all};
+    const int u_begin = mine.begin, u_end = mine.end;
 
     if (warp == kConsumers) {
         if (elect_one()) {
             prefetch_tensormap(&tmW);
             Giver give;
             bool ok = true;
-            int tile = steps ? (int)(u_begin / steps) : 0;
-            int64_t st = steps ? u_begin - tile * steps : 0;
-            int ai = (int)(st / ring.steps), q = (int)(st - (int64_t)ai * ring.steps);
-            for (int64_t u = u_begin; u < u_end && ok; u++) {
+            int tile = steps ? u_begin / steps : 0;
+            const int st = u_begin - tile * steps;
+            int ai = st / ring.steps, q = st - ai * ring.steps;
+            for (int u = u_begin; u < u_end && ok; u++) {
                 const int row = (int)R->expert[ai] * H + 32 * tile;
                 ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row, row + 16, q * ring.blocks * 2);
                 if (++q == ring.steps) {
@@ -627,11 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) give.give_up(S, ring.slots);
             dependency_wait();  // no CTA ends before the previous kernel has
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         }
         return;
     }
 
     dependency_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (all == 0) {  // no token has an expert
         for (int64_t i = (int64_t)blockIdx.x * 32 * kConsumers + threadIdx.x; i < (int64_t)T * H;
              i += (int64_t)gridDim.x * 32 * kConsumers)
@@ -707,17 +725,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     Taker take(S);
-    int tile = (int)(u_begin / steps);
-    int64_t st = u_begin - tile * steps;
-    int ai = (int)(st / ring.steps), q = (int)(st - (int64_t)ai * ring.steps);
+    int tile = u_begin / steps, st = u_begin - tile * steps;
+    int ai = st / ring.steps, q = st - ai * ring.steps;
     Next nx[2][MT];
     float sc_next = 0.0f;
     if (u_begin < u_end) load_step(ai, tile, q, nx, sc_next);
-    for (int64_t u = u_begin; u < u_end;) {
-        const int64_t first = st;
-        const int64_t count = min(steps - st, u_end - u);
+    for (int u = u_begin; u < u_end;) {
+        const int first = st, count = min(steps - st, u_end - u);
         float acc[TG][MT][4] = {};
-        for (int64_t k = 0; k < count; k++) {
+        for (int k = 0; k < count; k++) {
             uint32_t f[2][MT][8];
             const uint32_t mask = R->tokens[ai];
             const int8_t *sh = shift + ai * kMoeMaxTokens;
@@ -754,11 +770,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int b0 = 0, b1 = 0;
         if (first != 0 || st != steps) {
             // a shared tile: leave the sums, count, and add everybody's if last
-            const int64_t t0 = (int64_t)tile * steps;
-            b0 = (int)(((t0 + 1) * shares - 1) / all);
-            b1 = (int)(((t0 + steps) * shares - 1) / all);
-            float *mine = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kPart;
-            for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) __stcg(mine + v, sums[v]);
+            b0 = share_at(all, tile * steps, shares);
+            b1 = share_at(all, (tile + 1) * steps - 1, shares);
+            float *part = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kPart;
+            for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) __stcg(part + v, sums[v]);
             __threadfence();
             consumers_sync();
             if (threadIdx.x == 0) S->last = atomicAdd(ws.count + tile, 1) == b1 - b0;
@@ -773,8 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum = 0.0f;
                     for (int b = b0; b <= b1; b++) {
                         // a share's slot: 1 where it starts at the tile's first step
-                        const int64_t begin = all * b / shares;
-                        const int head = begin <= (int64_t)tile * steps;
+                        const int head = share_of(all, b, shares).begin <= tile * steps;
                         sum += __ldcg(ws.part + ((int64_t)b * 2 + head) * kPart + v);
                     }
                 }

@@ -100,7 +100,7 @@ def test_moe_pointer_refusals(i):
 def test_moe_workspace_query_refuses_bad_shapes():
     f = bsq.fp8_moe_workspace_bytes
     for bad in [(-1, 256, 128, 2), (17, 256, 128, 2), (4, 250, 128, 2), (4, 256, 130, 2), (4, 256, 128, 0),
-                (4, 256, 128, 17)]:
+                (4, 256, 128, 17), (4, 65536 + 128, 128, 2), (4, 256, 65536 + 128, 2)]:
         assert f(*bad) == 0
 
 
