@@ -51,19 +51,24 @@ constexpr int SB = 128;        // K of one scale block: two 64-byte chunks
 constexpr int kMaxSlots = 16;
 constexpr int kMaxActive = kMoeMaxTokens * kMoeMaxTopk;
 constexpr int kRed = 8192;     // floats of the warps' partial sums; the routing keys before that
-constexpr int kSums = 1024;    // floats of a group's sums: tiles x (8 or 16 tokens) x 16 rows, at most
-constexpr int kPart = 512;     // the down kernel's
-static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums, "shared buffer");
+constexpr int kSums = 512;     // floats of a group's sums: tiles x 16 rows x 8 columns
+constexpr int kPart = 512;     // of an output tile's: 32 rows x 16 tokens
+static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums && 2 * kMaxActive <= kSums,
+              "shared buffers");
 
 static __device__ unsigned int g_timeouts;
+
+constexpr uint32_t kNoColumn = 0xFFFFFFFFu;
 
 struct alignas(16) Route {
     float weight[kMoeMaxTokens][kMoeMaxTopk];
     uint16_t id[kMoeMaxTokens][kMoeMaxTopk];
-    uint32_t slot[kMoeMaxExperts];      // by expert: its tokens, then its place in `expert`
-    uint16_t expert[kMaxActive];        // the reached experts, in order
-    uint16_t tokens[kMaxActive];        // their tokens, a bit each
-    uint8_t pick[kMaxActive][kMoeMaxTokens];  // which of the token's choices the expert is
+    uint32_t slot[kMoeMaxExperts];     // by expert: its tokens, then its place in the list
+    // the reached experts, in order; one with more than eight tokens is listed
+    // twice, with its first eight and with the others
+    uint16_t expert[kMaxActive];
+    uint16_t tokens[kMaxActive];       // a bit each
+    uint32_t column[kMaxActive][8];    // its c-th token: (token << 16) | pair (token * topk + choice), or kNoColumn
     int warp_count[kMoeMaxExperts / 32];
     int active;
 };
@@ -106,14 +111,12 @@ __device__ __forceinline__ float route_exp(float l, float mx) {
 }
 
 // Routes every token (a warp each, in turn) and lists the reached experts.
-// SPLIT: an expert with more than eight tokens is listed twice, with its first
-// eight and with the others.
 // `keys`: kMoeMaxTokens x kMoeMaxExperts words.  Called by all threads of the
 // CTA.
-template <bool SPLIT>
 __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < kMoeMaxExperts; e += kThreads) R->slot[e] = 0;
+    for (int i = threadIdx.x; i < kMaxActive * 8; i += kThreads) R->column[0][i] = kNoColumn;
     __syncthreads();
     for (int t = warp; t < a.tokens; t += kThreads / 32) {
         // each lane's largest key and its lowest index
@@ -173,7 +176,7 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
         for (int i = 0; i < HALVES; i++) {
             mask[i] = R->slot[i * 32 * kConsumers + threadIdx.x];
             one[i] = __ballot_sync(0xFFFFFFFFu, mask[i] != 0);
-            two[i] = SPLIT ? __ballot_sync(0xFFFFFFFFu, __popc(mask[i]) > 8) : 0u;
+            two[i] = __ballot_sync(0xFFFFFFFFu, __popc(mask[i]) > 8);
             if (lane == 0) R->warp_count[i * kConsumers + warp] = __popc(one[i]) + __popc(two[i]);
         }
     }
@@ -186,8 +189,7 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
             const int before = lane < w ? R->warp_count[lane] : 0;  // (at most 16 warps' counts)
             const int at = (int)__reduce_add_sync(0xFFFFFFFFu, before) + __popc(one[i] & below) + __popc(two[i] & below);
             uint32_t first = mask[i];
-            if (SPLIT)
-                while (__popc(first) > 8) first &= ~(0x80000000u >> __clz(first));
+            while (__popc(first) > 8) first &= ~(0x80000000u >> __clz(first));
             if (mask[i]) {
                 R->expert[at] = (uint16_t)e;
                 R->tokens[at] = (uint16_t)first;
@@ -204,8 +206,8 @@ __device__ __forceinline__ void route(const MoeArgs &a, Route *R, uint32_t *keys
     const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
     if (t < a.tokens && j < a.topk && R->weight[t][j] > 0.0f) {
         int at = R->slot[R->id[t][j]];
-        if (SPLIT) at += !((R->tokens[at] >> t) & 1);
-        R->pick[at][t] = (uint8_t)j;
+        at += !((R->tokens[at] >> t) & 1);
+        R->column[at][__popc(R->tokens[at] & ((1u << t) - 1u))] = (uint32_t)(t << 16 | (t * a.topk + j));
     }
     __syncthreads();
 }
@@ -269,14 +271,12 @@ __device__ __forceinline__ void chunk_mma_8(float (&d)[4], const uint4 &wa, cons
     }
 }
 
-// The next slot: this warp's scale block (two chunks) of each of its two boxes
-// times the activation fragments x[chunk][token half], as independent chains
-// of MMAs, handed to `add` with its accumulator.  tokens: a half without any
-// is skipped.
-template <int MT, class Add>
+// The next slot: acc[box] += scale[box] * (this warp's scale block, two chunks,
+// of the slot's box) x the activation fragments x[chunk], as four independent
+// chains of MMAs.
 __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, int slot_bytes, int slots, bool active,
-                                         int warp, int lane, uint32_t tokens, const uint32_t (&x)[2][MT][8],
-                                         float (&acc0)[MT][4], float (&acc1)[MT][4], Add &&add) {
+                                         int warp, int lane, const uint32_t (&x)[2][8], const float (&scale)[2],
+                                         float (&acc0)[4], float (&acc1)[4]) {
     const uint32_t at = take.take(S, ring, slot_bytes) + warp * 2 * 16 * CH;
     const int g = lane >> 2, t = lane & 3;
     uint4 w[2][2][2];  // [box][chunk][row g, g + 8]
@@ -292,19 +292,15 @@ __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, in
     }
     take.give_back(slots, lane);
     if (!active) return;
+    float d[2][2][4] = {};  // [box][chunk]
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-        if (MT == 2 && ((tokens >> (8 * i)) & 0xFFu) == 0) continue;
-        float d[2][2][4] = {};  // [box][chunk]
+    for (int c = 0; c < 2; c++)
 #pragma unroll
-        for (int c = 0; c < 2; c++)
+        for (int v = 0; v < 2; v++) chunk_mma_8(d[v][c], w[v][c][0], w[v][c][1], x[c]);
 #pragma unroll
-            for (int v = 0; v < 2; v++) chunk_mma_8(d[v][c], w[v][c][0], w[v][c][1], x[c][i]);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            add(acc0[i][k], d[0][0][k] + d[0][1][k], 0, i, k);
-            add(acc1[i][k], d[1][0][k] + d[1][1][k], 1, i, k);
-        }
+    for (int k = 0; k < 4; k++) {
+        acc0[k] = __fmaf_rn(d[0][0][k] + d[0][1][k], scale[0], acc0[k]);
+        acc1[k] = __fmaf_rn(d[1][0][k] + d[1][1][k], scale[1], acc1[k]);
     }
 }
 
@@ -346,24 +342,21 @@ __device__ __forceinline__ void init_bars(Bars *S, int slots) {
     }
 }
 
-// The warps' partial sums of `n` outputs (n = tiles x MT x 128; an
-// output's index is ((tile * MT + token half) * 4 + r) * 32 + lane, as the MMA
-// leaves it), added in warp order.
-template <int TG, int MT>
-__device__ __forceinline__ void reduce_warps(const float (&acc)[TG][MT][4], float *red, float *sums, int warp, int lane,
+// The warps' partial sums of `n` outputs (an output's index is (tile * 4 + r)
+// * 32 + lane, as the MMA leaves it), added in warp order.
+template <int TG>
+__device__ __forceinline__ void reduce_warps(const float (&acc)[TG][4], float *red, float *sums, int warp, int lane,
                                              int n) {
     consumers_sync();  // the previous group's sums have been read
 #pragma unroll
     for (int u = 0; u < TG; u++)
 #pragma unroll
-        for (int i = 0; i < MT; i++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) red[(((warp * TG + u) * MT + i) * 4 + r) * 32 + lane] = acc[u][i][r];
+        for (int r = 0; r < 4; r++) red[((warp * TG + u) * 4 + r) * 32 + lane] = acc[u][r];
     consumers_sync();
     for (int v = threadIdx.x; v < n; v += 32 * kConsumers) {
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kConsumers; w++) sum += red[w * TG * MT * 128 + v];
+        for (int w = 0; w < kConsumers; w++) sum += red[w * TG * 128 + v];
         sums[v] = sum;
     }
     consumers_sync();
@@ -384,6 +377,9 @@ __device__ __forceinline__ int share_at(int all, int u, int g) {
     return u < more * (per + 1) ? u / (per + 1) : more + (u - more * (per + 1)) / per;
 }
 
+// The token of a column, -1 without one.
+__device__ __forceinline__ int token_of(uint32_t column) { return column == kNoColumn ? -1 : (int)(column >> 16); }
+
 // Workspace layout.
 struct Ws {
     __half *act;       // [tokens * topk, inter], times a power of two per 16
@@ -401,7 +397,7 @@ __device__ __forceinline__ int exp_shift(int e) { return e == 0 ? 127 : min(14 -
 //        (64, 16, 2 ring.blocks)
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_gate_up(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
-    constexpr int MT = 1, PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
+    constexpr int PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int slot_bytes = 2 * ring.blocks * 16 * SB;
@@ -419,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one writes before it has completed, and everything before this one has
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    route<true>(a, R, reinterpret_cast<uint32_t *>(red));
+    route(a, R, reinterpret_cast<uint32_t *>(red));
 
     // this CTA's share of the (expert, 16 rows) units
     const int per_expert = I >> 4;
@@ -449,12 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7;
-    // The MMA's columns are the listed expert's tokens, compactly: column c is
-    // its c-th token (-1 past the last).
-    auto column = [&](uint32_t mask, int c) {
-        for (int i = 0; i < c; i++) mask &= mask - 1;
-        return __ffs(mask) - 1;
-    };
     // this lane's activations of step q for token m, [chunk][16-byte half]:
     // zeros without a token and past the end of K
     auto load_x = [&](int m, int q, uint4(&x)[2][2]) {
@@ -485,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float nsc[TG];
     int m_next = -1, ai = u_begin / per_expert, r = u_begin - ai * per_expert;
     if (u_begin < u_end) {
-        m_next = column(R->tokens[ai], g);
+        m_next = token_of(R->column[ai][g]);
         load_x(m_next, 0, nx);
         load_scales(ai, r, 0, nsc);
     }
@@ -527,23 +517,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = u_begin; u < u_end;) {
         const int n = min(min(PG, per_expert - r), u_end - u);
         const int ai1 = r + n == per_expert ? ai + 1 : ai, r1 = r + n == per_expert ? 0 : r + n;  // the next group
-        const uint32_t mask = R->tokens[ai];
         const int my = m_next;  // this lane's token
         const float xs = pow2i(row_shift(S->rowmax[max(my, 0)]));
-        float acc[TG][MT][4] = {};
+        float acc[TG][4] = {};
         for (int q = 0; q < ring.steps; q++) {
-            uint32_t f[2][MT][8];
+            uint32_t f[2][8];
 #pragma unroll
-            for (int c = 0; c < 2; c++) x_to_f16<MT>(nx[c], xs, f[c][0]);
-            float sc[TG];
+            for (int c = 0; c < 2; c++) x_to_f16<1>(nx[c], xs, f[c]);
+            float sc[PG][2];
 #pragma unroll
-            for (int v = 0; v < TG; v++) sc[v] = nsc[v];
+            for (int v = 0; v < TG; v++) sc[v >> 1][v & 1] = nsc[v];
             // the next step's, one step ahead
             if (q + 1 < ring.steps) {
                 load_x(my, q + 1, nx);
                 load_scales(ai, r, q + 1, nsc);
             } else if (u + n < u_end) {
-                m_next = column(R->tokens[ai1], g);
+                m_next = token_of(R->column[ai1][g]);
                 load_x(m_next, 0, nx);
                 load_scales(ai1, r1, 0, nsc);
             }
@@ -551,17 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < PG; p++) {
                 if (p >= n) break;
-                slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, mask, f, acc[2 * p],
-                             acc[2 * p + 1],
-                             [&](float &o, float d, int v, int, int) { o = __fmaf_rn(d, sc[2 * p + v], o); });
+                slot_mma(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, sc[p], acc[2 * p],
+                         acc[2 * p + 1]);
             }
         }
-        reduce_warps<TG, MT>(acc, red, sums, warp, lane, 2 * n * MT * 128);
+        reduce_warps<TG>(acc, red, sums, warp, lane, 2 * n * 128);
         // silu(gate) * up: a warp takes one (pair, column parity), a lane rows
         // g and g + 8 of column 2 t + parity
         if (warp < 2 * n) {
             const int p = warp >> 1, c = warp & 1;
-            const int m = column(mask, 2 * t + c);
+            const uint32_t col = R->column[ai][2 * t + c];
+            const int m = token_of(col);
             const float unscale = pow2i(-row_shift(S->rowmax[max(m, 0)]));
             const float *gs = sums + (2 * p * 4 + c) * 32 + lane, *us = gs + 128;
             float v[2];
@@ -575,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
             if (m >= 0) {
-                const int64_t pair = (int64_t)m * a.topk + R->pick[ai][m];
+                const int64_t pair = col & 0xFFFFu;
                 const int ex = (int)(__float_as_uint(mx) >> 23);
                 const float s = pow2i(exp_shift(ex));
                 __half *dst = ws.act + pair * I + 16 * (r + p) + g;
@@ -593,27 +582,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -------------------------------------------------------------------- down --
 //   tmW  [experts * hidden] rows x inter, as (64 B, rows, inter / 64), box
 //        (64, 16, 2 ring.blocks)
-template <int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_down(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
-    constexpr int TG = 2;  // 16-row tiles sharing one pass over act
-    constexpr int OUTS = TG * MT * 128;
-    static_assert(OUTS <= kPart, "workspace sums");
+    constexpr int ROW = kMoeMaxTokens + 1;  // floats of an output row's sums (odd: rows fall into different banks)
+    constexpr int WARP_SUMS = 32 * ROW;
+    static_assert(kConsumers * WARP_SUMS <= kRed && 32 * kMoeMaxTokens == kPart, "sums of a tile");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int slot_bytes = 2 * ring.blocks * 16 * SB;
     float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
     float *sums = red + kRed;
-    float *coef = sums + kSums;  // [active][tokens]: routing weight x the undone power of two
-    Route *R = reinterpret_cast<Route *>(coef + kMaxActive * kMoeMaxTokens);
+    float *coef = sums;  // [pair]: routing weight x the undone power of two
+    Route *R = reinterpret_cast<Route *>(sums + kSums);
     Bars *S = reinterpret_cast<Bars *>(R + 1);
-    int8_t *shift = reinterpret_cast<int8_t *>(S + 1);  // [active][tokens]: the row's power of two
+    int8_t *shift = reinterpret_cast<int8_t *>(sums + kMaxActive);  // [pair]: its row's power of two
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.hidden, I = a.inter, T = a.tokens;
     init_bars(S, ring.slots);
     __syncthreads();
-    route<false>(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
+    route(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
 
     // this CTA's share of the (32-row tile, expert, K step) sequence; no share
     // is empty, which the count of a shared tile's shares relies on
@@ -670,9 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = __vmaxu4(mx, mx >> 16);
         mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu));
         if (lane == 0) {
-            const int s = exp_shift((int)mx), at = (int)R->slot[R->id[m][j]] * kMoeMaxTokens + m;
-            shift[at] = (int8_t)s;
-            coef[at] = w * pow2i(-s);
+            const int s = exp_shift((int)mx);
+            shift[p] = (int8_t)s;
+            coef[p] = w * pow2i(-s);
         }
     }
     consumers_sync();
@@ -680,145 +668,175 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7, ib = I >> 7;
-    struct Next {
-        uint4 v[2];
-        int ex;  // -1: no such token here
+    // A step's input of this lane: its token's act, 2 x 16 FP16 values, their
+    // groups' exponents, and the scale of this warp's block.
+    struct Input {
+        uint4 v[2][2];
+        int ex[2];
+        float sc;
     };
-    // act of token m for expert place ai at K offset k: sixteen FP16 values
-    // and their group's exponent
-    auto load_act = [&](int ai, int m, int k, bool in, Next &o) {
-        in = in && ((R->tokens[ai] >> m) & 1);
-        o.v[0] = o.v[1] = make_uint4(0u, 0u, 0u, 0u);
-        o.ex = -1;
-        if (in) {
-            const int64_t pair = (int64_t)m * a.topk + R->pick[ai][m];
-            const uint4 *src = reinterpret_cast<const uint4 *>(ws.act + pair * I + k);
-            o.v[0] = __ldcg(src);
-            o.v[1] = __ldcg(src + 1);
-            o.ex = __ldcg(ws.act_exp + pair * (I >> 4) + (k >> 4));
+    // a place in the sequence
+    struct Pos {
+        int tile, ai, q;
+    };
+    auto advance = [&](Pos &p) {
+        if (++p.q == ring.steps) {
+            p.q = 0;
+            if (++p.ai == R->active) {
+                p.ai = 0;
+                p.tile++;
+            }
         }
     };
-    // brought to the row's power of two: a factor of 2^-d, exact down to
+    auto load = [&](const Pos &p, Input &o) {
+        const int kb = p.q * ring.blocks + warp;
+        const bool in = warp < ring.blocks && kb < ib;
+        const uint32_t col = R->column[p.ai][g];
+        const bool some = in && col != kNoColumn;
+        const int64_t pair = some ? col & 0xFFFFu : 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(ws.act + pair * I + kb * SB + 16 * t);
+        const uint8_t *ex = ws.act_exp + pair * (I >> 4) + 8 * kb + t;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            o.v[c][0] = some ? __ldcg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+            o.v[c][1] = some ? __ldcg(src + 8 * c + 1) : make_uint4(0u, 0u, 0u, 0u);
+            o.ex[c] = some ? __ldcg(ex + 4 * c) : -1;
+        }
+        // the tile's 32 rows lie in one scale block
+        o.sc = in ? __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + (p.tile >> 2)) * ib + kb) : 0.0f;
+    };
+    // act brought to its row's power of two: a factor of 2^-d, exact down to
     // FP16's subnormals
-    auto to_row = [&](const Next &n, int row_shift_, uint32_t(&o)[8]) {
-        const int d = n.ex < 0 ? 25 : exp_shift(n.ex) - row_shift_;  // >= 0
+    auto to_row = [&](const uint4(&v)[2], int ex, int row_exp, uint32_t(&o)[8]) {
+        const int d = ex < 0 ? 25 : exp_shift(ex) - row_exp;  // >= 0
         const __half f = d > 24 ? __ushort_as_half((unsigned short)0)
                                 : (d <= 14 ? __ushort_as_half((unsigned short)((15 - d) << 10))
                                            : __ushort_as_half((unsigned short)(1 << (24 - d))));
         const __half2 f2 = __half2half2(f);
-        const uint32_t w[8] = {n.v[0].x, n.v[0].y, n.v[0].z, n.v[0].w, n.v[1].x, n.v[1].y, n.v[1].z, n.v[1].w};
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&w[j]), f2);
             o[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
     };
-    auto load_step = [&](int ai, int tile, int q, Next(&n)[2][MT], float &sc) {
-        const int kb = q * ring.blocks + warp;
-        const bool in = warp < ring.blocks && kb < ib;
-#pragma unroll
-        for (int c = 0; c < 2; c++)
-#pragma unroll
-            for (int i = 0; i < MT; i++) load_act(ai, g + 8 * i, kb * SB + CH * c + 16 * t, in, n[c][i]);
-        // the tile's 32 rows lie in one scale block
-        sc = in ? __ldg(a.s_d + ((int64_t)R->expert[ai] * hb + (tile >> 2)) * ib + kb) : 0.0f;
-    };
 
+    // This warp's sums of the tile, [row][token]; an expert's products gather
+    // in registers over its K steps and are added here, weighted, per token.
+    float *own = red + warp * WARP_SUMS;
+    auto clear = [&] {
+        for (int i = lane; i < WARP_SUMS; i += 32) own[i] = 0.0f;
+        __syncwarp();
+    };
     Taker take(S);
-    int tile = u_begin / steps, st = u_begin - tile * steps;
-    int ai = st / ring.steps, q = st - ai * ring.steps;
-    Next nx[2][MT];
-    float sc_next = 0.0f;
-    if (u_begin < u_end) load_step(ai, tile, q, nx, sc_next);
-    for (int u = u_begin; u < u_end;) {
-        const int first = st, count = min(steps - st, u_end - u);
-        float acc[TG][MT][4] = {};
-        for (int k = 0; k < count; k++) {
-            uint32_t f[2][MT][8];
-            const uint32_t mask = R->tokens[ai];
-            const int8_t *sh = shift + ai * kMoeMaxTokens;
+    Pos cur, ahead;
+    cur.tile = u_begin / steps;
+    const int st = u_begin - cur.tile * steps;
+    cur.ai = st / ring.steps;
+    cur.q = st - cur.ai * ring.steps;
+    int first = st;  // the tile's first step here
+    float acc[2][4] = {};
+    clear();
+    // two steps ahead: one lasts about as long as the way to L2 and back
+    Input in0, in1;
+    ahead = cur;
+    if (u_begin < u_end) load(ahead, in0);
+    advance(ahead);
+    if (u_begin + 1 < u_end) load(ahead, in1);
+    advance(ahead);
+    // The tile's sums over the warps, in warp order.  A tile shared with other
+    // CTAs: leave them in the workspace, count, and add everybody's if last.
+    auto finish_tile = [&](int tile, bool shared) {
+        consumers_sync();
+        float sum[2];
 #pragma unroll
-            for (int c = 0; c < 2; c++)
+        for (int h = 0; h < 2; h++) {
+            const int v = threadIdx.x + h * 32 * kConsumers;
+            sum[h] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < MT; i++) to_row(nx[c][i], sh[g + 8 * i], f[c][i]);
-            const float sc = sc_next;
-            float cf[MT][2];
-#pragma unroll
-            for (int i = 0; i < MT; i++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    const int m = 8 * i + 2 * t + c;
-                    cf[i][c] = ((mask >> m) & 1) ? coef[ai * kMoeMaxTokens + m] * sc : 0.0f;
-                }
-            const bool active = warp < ring.blocks && q * ring.blocks + warp < ib;
-            int tile1 = tile;
-            if (++q == ring.steps) {
-                q = 0;
-                if (++ai == R->active) {
-                    ai = 0;
-                    tile1++;
-                }
-            }
-            if (u + k + 1 < u_end) load_step(ai, tile1, q, nx, sc_next);
-            slot_mma<MT>(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, mask, f, acc[0], acc[1],
-                         [&](float &o, float d, int, int i, int r) { o = __fmaf_rn(d, cf[i][r & 1], o); });
+            for (int w = 0; w < kConsumers; w++) sum[h] += red[w * WARP_SUMS + (v >> 4) * ROW + (v & 15)];
         }
-        reduce_warps<TG, MT>(acc, red, sums, warp, lane, OUTS);
-        u += count;
-        st += count;
-        bool finish = true;
-        int b0 = 0, b1 = 0;
-        if (first != 0 || st != steps) {
-            // a shared tile: leave the sums, count, and add everybody's if last
-            b0 = share_at(all, tile * steps, shares);
-            b1 = share_at(all, (tile + 1) * steps - 1, shares);
+        if (shared) {
+            const int b0 = share_at(all, tile * steps, shares), b1 = share_at(all, (tile + 1) * steps - 1, shares);
             float *part = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kPart;
-            for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) __stcg(part + v, sums[v]);
+#pragma unroll
+            for (int h = 0; h < 2; h++) __stcg(part + threadIdx.x + h * 32 * kConsumers, sum[h]);
             __threadfence();
             consumers_sync();
             if (threadIdx.x == 0) S->last = atomicAdd(ws.count + tile, 1) == b1 - b0;
             consumers_sync();
-            finish = S->last != 0;
-            if (finish) __threadfence();
-        }
-        if (finish) {
-            for (int v = threadIdx.x; v < OUTS; v += 32 * kConsumers) {
-                float sum = sums[v];
-                if (b1 > b0) {
-                    sum = 0.0f;
-                    for (int b = b0; b <= b1; b++) {
-                        // a share's slot: 1 where it starts at the tile's first step
-                        const int head = share_of(all, b, shares).begin <= tile * steps;
-                        sum += __ldcg(ws.part + ((int64_t)b * 2 + head) * kPart + v);
-                    }
+            if (S->last) {
+                __threadfence();
+                sum[0] = sum[1] = 0.0f;
+                for (int b = b0; b <= b1; b++) {
+                    // a share's slot: 1 where it has the tile's first step
+                    const int head = share_of(all, b, shares).begin <= tile * steps;
+                    const float *p = ws.part + ((int64_t)b * 2 + head) * kPart + threadIdx.x;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) sum[h] += __ldcg(p + h * 32 * kConsumers);
                 }
-                const int w = v / (MT * 128), i = (v >> 7) % MT, r = (v >> 5) & 3, ln = v & 31;
-                const int n = 32 * tile + 16 * w + (ln >> 2) + 8 * (r >> 1), m = 8 * i + 2 * (ln & 3) + (r & 1);
-                if (m < T) a.out[(int64_t)m * H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
             }
         }
-        if (st == steps) {
-            st = 0;
-            tile++;
+        if (!shared || S->last) {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int v = threadIdx.x + h * 32 * kConsumers, m = v & 15;
+                if (m < T) a.out[(int64_t)m * H + 32 * tile + (v >> 4)] = __bfloat16_as_ushort(__float2bfloat16_rn(sum[h]));
+            }
         }
+        consumers_sync();  // everybody's sums, and the flag, have been read
+        clear();
+    };
+    auto step = [&](Input &in, int u) {
+        const uint32_t col = R->column[cur.ai][g];
+        const int row_exp = col == kNoColumn ? 0 : shift[col & 0xFFFFu];
+        uint32_t f[2][8];
+#pragma unroll
+        for (int c = 0; c < 2; c++) to_row(in.v[c], in.ex[c], row_exp, f[c]);
+        const float sc[2] = {in.sc, in.sc};
+        if (u + 2 < u_end) load(ahead, in);
+        advance(ahead);
+        const bool active = warp < ring.blocks && cur.q * ring.blocks + warp < ib;
+        slot_mma(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, sc, acc[0], acc[1]);
+        const int tile = cur.tile, ai = cur.ai;
+        advance(cur);
+        if (cur.ai == ai && cur.tile == tile && u + 1 < u_end) return;
+        // the expert's last step here: columns 2t and 2t + 1, rows g and g + 8
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            const uint32_t to = R->column[ai][2 * t + c];
+            if (to != kNoColumn) {
+                const float cf = coef[to & 0xFFFFu];
+                float *o = own + g * ROW + (to >> 16);
+#pragma unroll
+                for (int r = 0; r < 4; r++) o[8 * r * ROW] = __fmaf_rn(acc[r >> 1][2 * (r & 1) + c], cf, o[8 * r * ROW]);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 4; r++) acc[0][r] = acc[1][r] = 0.0f;
+        if (cur.tile == tile && u + 1 < u_end) return;
+        finish_tile(tile, first != 0 || cur.tile == tile);
+        first = 0;
+    };
+    for (int u = u_begin; u < u_end; u += 2) {
+        step(in0, u);
+        if (u + 1 < u_end) step(in1, u + 1);
     }
 }
 
 // -------------------------------------------------------------------- host --
 
 constexpr size_t kSmemMax = 232448;
-constexpr size_t gate_up_fixed() { return 1024 + (kRed + kSums) * 4 + sizeof(Route) + sizeof(Bars); }
-constexpr size_t down_fixed() {
-    return gate_up_fixed() + (size_t)kMaxActive * kMoeMaxTokens * (sizeof(float) + 1);
-}
+constexpr size_t kFixed = 1024 + (kRed + kSums) * 4 + sizeof(Route) + sizeof(Bars);  // all but the ring
 
 // Boxes of equal size, at most 1 KB of K, and as many slots as fit.
-Ring ring_for(int k, size_t fixed) {
+Ring ring_for(int k) {
     Ring r;
     const int blocks = k / SB;
     r.steps = (blocks + kConsumers - 1) / kConsumers;
     r.blocks = (blocks + r.steps - 1) / r.steps;
-    const int room = (int)((kSmemMax - fixed) / ((size_t)r.blocks * 2 * 16 * SB));
+    const int room = (int)((kSmemMax - kFixed) / ((size_t)r.blocks * 2 * 16 * SB));
     r.slots = room < kMaxSlots ? room : kMaxSlots;
     return r;
 }
@@ -841,8 +859,8 @@ size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
 }
 
 template <class F>
-cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Ring &ring, size_t smem, const MoeArgs &a,
-                       const Ws &ws, cudaStream_t s) {
+cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const MoeArgs &a, const Ws &ws, cudaStream_t s) {
+    const Ring ring = ring_for(k);
     alignas(64) CUtensorMap tm;
     const uint64_t d[3] = {CH, (uint64_t)rows, (uint64_t)k / CH}, st[2] = {(uint64_t)k, CH};
     const uint32_t box[3] = {CH, 16, (uint32_t)(2 * ring.blocks)};
@@ -850,7 +868,7 @@ cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Ri
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sm_count());
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kFixed + (size_t)ring.slots * ring.blocks * 2 * 16 * SB;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -860,25 +878,6 @@ cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Ri
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tm, a, ring, ws);
     if (e == cudaSuccess) note_launch();
     return e;
-}
-
-template <int MT> cudaError_t launch_mt(const MoeArgs &a, cudaStream_t s) {
-    static DeviceOnce attrs;
-    cudaError_t e = attrs.run([] {
-        const cudaError_t err = cudaFuncSetAttribute(k_moe_gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     (int)kSmemMax);
-        if (err != cudaSuccess) return err;
-        return cudaFuncSetAttribute(k_moe_down<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
-    });
-    if (e != cudaSuccess) return e;
-    Ws ws;
-    ws_layout(a.workspace, a.tokens, a.hidden, a.inter, a.topk, &ws);
-    const Ring up = ring_for(a.hidden, gate_up_fixed()), down = ring_for(a.inter, down_fixed());
-    e = launch_one(k_moe_gate_up, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, up,
-                   gate_up_fixed() + (size_t)up.slots * up.blocks * 2 * 16 * SB, a, ws, s);
-    if (e != cudaSuccess) return e;
-    return launch_one(k_moe_down<MT>, a.w_d, (int64_t)a.experts * a.hidden, a.inter, down,
-                      down_fixed() + (size_t)down.slots * down.blocks * 2 * 16 * SB, a, ws, s);
 }
 
 }  // namespace
@@ -895,7 +894,19 @@ size_t fp8_moe_workspace_bytes(int tokens, int hidden, int inter, int topk) {
 }
 
 cudaError_t launch_fp8_moe_blockscaled(const MoeArgs &a, cudaStream_t s) {
-    return a.tokens <= 8 ? launch_mt<1>(a, s) : launch_mt<2>(a, s);
+    static DeviceOnce attrs;
+    cudaError_t e = attrs.run([] {
+        const cudaError_t err =
+            cudaFuncSetAttribute(k_moe_gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+        if (err != cudaSuccess) return err;
+        return cudaFuncSetAttribute(k_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    });
+    if (e != cudaSuccess) return e;
+    Ws ws;
+    ws_layout(a.workspace, a.tokens, a.hidden, a.inter, a.topk, &ws);
+    e = launch_one(k_moe_gate_up, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, a, ws, s);
+    if (e != cudaSuccess) return e;
+    return launch_one(k_moe_down, a.w_d, (int64_t)a.experts * a.hidden, a.inter, a, ws, s);
 }
 
 }  // namespace bsq
