@@ -18,7 +18,7 @@
 //                  and one of up rows give silu(g) * u on the spot.  act is
 //                  kept as FP16 times a power of two per 16 values, 11
 //                  significant bits.
-//   k_moe_down     an output tile of 32 rows runs over all reached experts'
+//   k_moe_down     an output tile of 64 rows runs over all reached experts'
 //                  K, so a token's experts add up in registers.  The (tile,
 //                  expert, K) steps are cut into equal shares, one per CTA,
 //                  also inside a tile: 448 tiles on 148 SMs would otherwise
@@ -50,9 +50,10 @@ constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int SB = 128;        // K of one scale block: two 64-byte chunks
 constexpr int kMaxSlots = 16;
 constexpr int kMaxActive = kMoeMaxTokens * kMoeMaxTopk;
-constexpr int kRed = 8192;     // floats of the warps' partial sums; the routing keys before that
+constexpr int kRed = 8704;     // floats of the warps' partial sums; the routing keys before that
 constexpr int kSums = 512;     // floats of a group's sums: tiles x 16 rows x 8 columns
-constexpr int kPart = 512;     // of an output tile's: 32 rows x 16 tokens
+constexpr int kTile = 64;      // rows of an output tile: two slots per step
+constexpr int kPart = kTile * kMoeMaxTokens;  // floats of an output tile's sums
 static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums && 2 * kMaxActive <= kSums,
               "shared buffers");
 
@@ -384,7 +385,7 @@ __device__ __forceinline__ int token_of(uint32_t column) { return column == kNoC
 struct Ws {
     __half *act;       // [tokens * topk, inter], times a power of two per 16
     uint8_t *act_exp;  // [tokens * topk, inter / 16]: exponent field of the 16 values' largest
-    int *count;        // [hidden / 32] shares of a tile that have come
+    int *count;        // [hidden / kTile] shares of a tile that have come
     float *part;       // [CTAs][2][kPart] FP32 sums of shared tiles
 };
 
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.topk_ids) a.topk_ids[t * a.topk + j] = R->id[t][j];
             if (a.topk_weights) a.topk_weights[t * a.topk + j] = R->weight[t][j];
         }
-        for (int i = threadIdx.x; i < (H >> 5); i += 32 * kConsumers) ws.count[i] = 0;
+        for (int i = threadIdx.x; i < H / kTile; i += 32 * kConsumers) ws.count[i] = 0;
     }
 
     consumers_sync();
@@ -585,8 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_down(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
     constexpr int ROW = kMoeMaxTokens + 1;  // floats of an output row's sums (odd: rows fall into different banks)
-    constexpr int WARP_SUMS = 32 * ROW;
-    static_assert(kConsumers * WARP_SUMS <= kRed && 32 * kMoeMaxTokens == kPart, "sums of a tile");
+    constexpr int WARP_SUMS = kTile * ROW, PER = kPart / (32 * kConsumers);
+    static_assert(kConsumers * WARP_SUMS <= kRed && PER * 32 * kConsumers == kPart, "sums of a tile");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int slot_bytes = 2 * ring.blocks * 16 * SB;
@@ -603,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     route(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
 
-    // this CTA's share of the (32-row tile, expert, K step) sequence; no share
+    // this CTA's share of the (64-row tile, expert, K step) sequence; no share
     // is empty, which the count of a shared tile's shares relies on
-    const int steps = R->active * ring.steps, all = steps * (H >> 5);  // of one tile, of all
+    const int steps = R->active * ring.steps, all = steps * (H / kTile);  // of one tile, of all
     const int shares = max(min((int)gridDim.x, all), 1);
     const Share mine = (int)blockIdx.x < shares ? share_of(all, blockIdx.x, shares) : Share{all, all};
     const int u_begin = mine.begin, u_end = mine.end;
@@ -619,8 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = u_begin - tile * steps;
             int ai = st / ring.steps, q = st - ai * ring.steps;
             for (int u = u_begin; u < u_end && ok; u++) {
-                const int row = (int)R->expert[ai] * H + 32 * tile;
-                ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row, row + 16, q * ring.blocks * 2);
+                const int row = (int)R->expert[ai] * H + kTile * tile;
+                for (int h = 0; h < kTile / 32 && ok; h++)
+                    ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 32 * h, row + 32 * h + 16,
+                                   q * ring.blocks * 2);
                 if (++q == ring.steps) {
                     q = 0;
                     if (++ai == R->active) {
@@ -702,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             o.v[c][1] = some ? __ldcg(src + 8 * c + 1) : make_uint4(0u, 0u, 0u, 0u);
             o.ex[c] = some ? __ldcg(ex + 4 * c) : -1;
         }
-        // the tile's 32 rows lie in one scale block
-        o.sc = in ? __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + (p.tile >> 2)) * ib + kb) : 0.0f;
+        // the tile's rows lie in one scale block
+        o.sc = in ? __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * kTile / 128) * ib + kb) : 0.0f;
     };
     // act brought to its row's power of two: a factor of 2^-d, exact down to
     // FP16's subnormals
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cur.ai = st / ring.steps;
     cur.q = st - cur.ai * ring.steps;
     int first = st;  // the tile's first step here
-    float acc[2][4] = {};
+    float acc[kTile / 16][4] = {};
     clear();
     // two steps ahead: one lasts about as long as the way to L2 and back
     Input in0, in1;
@@ -748,9 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // CTAs: leave them in the workspace, count, and add everybody's if last.
     auto finish_tile = [&](int tile, bool shared) {
         consumers_sync();
-        float sum[2];
+        float sum[PER];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int h = 0; h < PER; h++) {
             const int v = threadIdx.x + h * 32 * kConsumers;
             sum[h] = 0.0f;
 #pragma unroll
@@ -760,28 +763,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b0 = share_at(all, tile * steps, shares), b1 = share_at(all, (tile + 1) * steps - 1, shares);
             float *part = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kPart;
 #pragma unroll
-            for (int h = 0; h < 2; h++) __stcg(part + threadIdx.x + h * 32 * kConsumers, sum[h]);
+            for (int h = 0; h < PER; h++) __stcg(part + threadIdx.x + h * 32 * kConsumers, sum[h]);
             __threadfence();
             consumers_sync();
             if (threadIdx.x == 0) S->last = atomicAdd(ws.count + tile, 1) == b1 - b0;
             consumers_sync();
             if (S->last) {
                 __threadfence();
-                sum[0] = sum[1] = 0.0f;
+#pragma unroll
+                for (int h = 0; h < PER; h++) sum[h] = 0.0f;
                 for (int b = b0; b <= b1; b++) {
                     // a share's slot: 1 where it has the tile's first step
                     const int head = share_of(all, b, shares).begin <= tile * steps;
                     const float *p = ws.part + ((int64_t)b * 2 + head) * kPart + threadIdx.x;
 #pragma unroll
-                    for (int h = 0; h < 2; h++) sum[h] += __ldcg(p + h * 32 * kConsumers);
+                    for (int h = 0; h < PER; h++) sum[h] += __ldcg(p + h * 32 * kConsumers);
                 }
             }
         }
         if (!shared || S->last) {
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < PER; h++) {
                 const int v = threadIdx.x + h * 32 * kConsumers, m = v & 15;
-                if (m < T) a.out[(int64_t)m * H + 32 * tile + (v >> 4)] = __bfloat16_as_ushort(__float2bfloat16_rn(sum[h]));
+                if (m < T) a.out[(int64_t)m * H + kTile * tile + (v >> 4)] = __bfloat16_as_ushort(__float2bfloat16_rn(sum[h]));
             }
         }
         consumers_sync();  // everybody's sums, and the flag, have been read
@@ -797,7 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u + 2 < u_end) load(ahead, in);
         advance(ahead);
         const bool active = warp < ring.blocks && cur.q * ring.blocks + warp < ib;
-        slot_mma(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, sc, acc[0], acc[1]);
+#pragma unroll
+        for (int h = 0; h < kTile / 32; h++)
+            slot_mma(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, sc, acc[2 * h], acc[2 * h + 1]);
         const int tile = cur.tile, ai = cur.ai;
         advance(cur);
         if (cur.ai == ai && cur.tile == tile && u + 1 < u_end) return;
@@ -809,12 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float cf = coef[to & 0xFFFFu];
                 float *o = own + g * ROW + (to >> 16);
 #pragma unroll
-                for (int r = 0; r < 4; r++) o[8 * r * ROW] = __fmaf_rn(acc[r >> 1][2 * (r & 1) + c], cf, o[8 * r * ROW]);
+                for (int r = 0; r < kTile / 8; r++) o[8 * r * ROW] = __fmaf_rn(acc[r >> 1][2 * (r & 1) + c], cf, o[8 * r * ROW]);
             }
         }
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < 4; r++) acc[0][r] = acc[1][r] = 0.0f;
+        for (int r = 0; r < kTile / 16; r++) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
         if (cur.tile == tile && u + 1 < u_end) return;
         finish_tile(tile, first != 0 || cur.tile == tile);
         first = 0;
@@ -846,7 +852,7 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
     const size_t pairs = (size_t)tokens * topk;
     const size_t act = align256(pairs * inter * sizeof(__half)), ex = align256(pairs * (inter / 16)),
-                 count = align256((size_t)hidden / 32 * sizeof(int)),
+                 count = align256((size_t)hidden / kTile * sizeof(int)),
                  part = (size_t)sm_count() * 2 * kPart * sizeof(float);
     if (ws) {
         uint8_t *b = static_cast<uint8_t *>(p);
