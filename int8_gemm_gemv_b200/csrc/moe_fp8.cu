@@ -54,7 +54,7 @@ constexpr int kRed = 8704;     // floats of the warps' partial sums; the routing
 constexpr int kSums = 512;     // floats of a group's sums: tiles x 16 rows x 8 columns
 constexpr int kTile = 64;      // rows of an output tile: two slots per step
 constexpr int kPart = kTile * kMoeMaxTokens;  // floats of an output tile's sums
-static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums && 2 * kMaxActive <= kSums,
+static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums && 2 * kMaxActive <= kSums && kMaxActive + 1 <= 4 * (kSums - kMaxActive),
               "shared buffers");
 
 static __device__ unsigned int g_timeouts;
@@ -383,15 +383,15 @@ __device__ __forceinline__ int token_of(uint32_t column) { return column == kNoC
 
 // Workspace layout.
 struct Ws {
-    __half *act;       // [tokens * topk, inter], times a power of two per 16
-    uint8_t *act_exp;  // [tokens * topk, inter / 16]: exponent field of the 16 values' largest
+    __half *act;       // [tokens * topk + 1, inter], times a power of two per 16; the last row is zeros
+    uint8_t *act_exp;  // [tokens * topk + 1, inter / 16]: exponent field of the 16 values' largest
     int *count;        // [hidden / kTile] shares of a tile that have come
     float *part;       // [CTAs][2][kPart] FP32 sums of shared tiles
 };
 
 // The power of two for 16 (or a row of) act values whose largest has this
 // FP32 exponent field: brings it to [2^14, 2^15).
-__device__ __forceinline__ int exp_shift(int e) { return e == 0 ? 127 : min(14 - (e - 127), 127); }
+__device__ __forceinline__ int exp_shift(int e) { return min(14 - (e - 127), 127); }
 
 // ---------------------------------------------------------------- gate, up --
 //   tmW  [experts * 2 inter] rows x hidden, as (64 B, rows, hidden / 64), box
@@ -446,29 +446,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7;
-    // this lane's activations of step q for token m, [chunk][16-byte half]:
-    // zeros without a token and past the end of K
+    // this lane's activations of step q for token m, [chunk][16-byte half]
+    // (without a token, and past the end of K, some other valid ones: they are
+    // multiplied by zero, or not used; no branch)
     auto load_x = [&](int m, int q, uint4(&x)[2][2]) {
-        const int k = (q * ring.blocks + warp) * SB;
-        const bool in = m >= 0 && warp < ring.blocks && k < H;
-        const uint16_t *p = a.x + (int64_t)max(m, 0) * H + k + 16 * t;
+        const int kb = min(q * ring.blocks + warp, hb - 1);
+        const uint16_t *p = a.x + (int64_t)max(m, 0) * H + kb * SB + 16 * t;
 #pragma unroll
         for (int c = 0; c < 2; c++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) x[c][h] = in ? ldg_nc_v4(p + CH * c + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
+            for (int h = 0; h < 2; h++) x[c][h] = ldg_nc_v4(p + CH * c + 8 * h);
     };
     // the scales of this warp's block of step q for the group that starts at row
     // unit r of the listed expert ai (a unit's 16 rows lie in one scale block;
     // a group's may not)
     auto load_scales = [&](int ai, int r, int q, float(&sc)[TG]) {
-        const int kb = q * ring.blocks + warp;
-        const bool in = warp < ring.blocks && kb < hb;
+        const int kb = min(q * ring.blocks + warp, hb - 1);
 #pragma unroll
         for (int p = 0; p < PG; p++) {
             const int64_t row = (int64_t)R->expert[ai] * 2 * I + 16 * min(r + p, per_expert - 1);
             const float *s = a.s_gu + (row >> 7) * hb + kb;
-            sc[2 * p] = in ? __ldg(s) : 0.0f;
-            sc[2 * p + 1] = in ? __ldg(s + (int64_t)(I >> 7) * hb) : 0.0f;
+            sc[2 * p] = __ldg(s);
+            sc[2 * p + 1] = __ldg(s + (int64_t)(I >> 7) * hb);
         }
     };
     Taker take(S);
@@ -512,6 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.topk_weights) a.topk_weights[t * a.topk + j] = R->weight[t][j];
         }
         for (int i = threadIdx.x; i < H / kTile; i += 32 * kConsumers) ws.count[i] = 0;
+        // the row of zeros that columns without a token read
+        const int64_t none = (int64_t)T * a.topk;
+        for (int i = threadIdx.x; i < (I >> 3); i += 32 * kConsumers)
+            reinterpret_cast<uint4 *>(ws.act + none * I)[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = threadIdx.x; i < (I >> 4); i += 32 * kConsumers) ws.act_exp[none * (I >> 4) + i] = 0;
     }
 
     consumers_sync();
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = min(min(PG, per_expert - r), u_end - u);
         const int ai1 = r + n == per_expert ? ai + 1 : ai, r1 = r + n == per_expert ? 0 : r + n;  // the next group
         const int my = m_next;  // this lane's token
-        const float xs = pow2i(row_shift(S->rowmax[max(my, 0)]));
+        const float xs = my < 0 ? 0.0f : pow2i(row_shift(S->rowmax[my]));
         float acc[TG][4] = {};
         for (int q = 0; q < ring.steps; q++) {
             uint32_t f[2][8];
@@ -648,22 +652,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     // every (token, choice)'s power of two, from its groups' exponents
-    for (int p = warp; p < T * a.topk; p += kConsumers) {
-        const int m = p / a.topk, j = p - m * a.topk;
-        const float w = R->weight[m][j];
-        if (!(w > 0.0f)) continue;
-        const uint2 *ex = reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)p * (I >> 4));
-        uint32_t mx = 0;
-        for (int i = lane; i < (I >> 7); i += 32) {
-            const uint2 v = __ldcg(ex + i);
-            mx = __vmaxu4(mx, __vmaxu4(v.x, v.y));
+    const int none = T * a.topk;  // the row of zeros
+    if (threadIdx.x == 0) shift[none] = 0;
+    constexpr int PB = 4;  // pairs of a warp whose loads are in flight together
+    for (int p0 = warp; p0 < none; p0 += PB * kConsumers) {
+        uint32_t mx[PB];
+#pragma unroll
+        for (int i = 0; i < PB; i++) mx[i] = 0;
+        for (int k = lane; k < (I >> 7); k += 32) {
+            uint2 v[PB];
+#pragma unroll
+            for (int i = 0; i < PB; i++) {
+                const int p = min(p0 + i * kConsumers, none - 1);
+                v[i] = __ldcg(reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)p * (I >> 4)) + k);
+            }
+#pragma unroll
+            for (int i = 0; i < PB; i++) mx[i] = __vmaxu4(mx[i], __vmaxu4(v[i].x, v[i].y));
         }
-        mx = __vmaxu4(mx, mx >> 16);
-        mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu));
-        if (lane == 0) {
-            const int s = exp_shift((int)mx);
-            shift[p] = (int8_t)s;
-            coef[p] = w * pow2i(-s);
+#pragma unroll
+        for (int i = 0; i < PB; i++) {
+            const int p = p0 + i * kConsumers;
+            mx[i] = __vmaxu4(mx[i], mx[i] >> 16);
+            mx[i] = __reduce_max_sync(0xFFFFFFFFu, max(mx[i] & 0xFFu, (mx[i] >> 8) & 0xFFu));
+            // (a pair of weight 0 has no act, and no column refers to it)
+            if (lane == 0 && p < none) {
+                const int s = exp_shift((int)mx[i]);
+                shift[p] = (int8_t)s;
+                coef[p] = R->weight[p / a.topk][p % a.topk] * pow2i(-s);
+            }
         }
     }
     consumers_sync();
@@ -692,29 +708,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
     auto load = [&](const Pos &p, Input &o) {
-        const int kb = p.q * ring.blocks + warp;
-        const bool in = warp < ring.blocks && kb < ib;
+        // (past the end of K some other valid values, not used; no branch)
+        const int kb = min(p.q * ring.blocks + warp, ib - 1);
         const uint32_t col = R->column[p.ai][g];
-        const bool some = in && col != kNoColumn;
-        const int64_t pair = some ? col & 0xFFFFu : 0;
-        const uint4 *src = reinterpret_cast<const uint4 *>(ws.act + pair * I + kb * SB + 16 * t);
-        const uint8_t *ex = ws.act_exp + pair * (I >> 4) + 8 * kb + t;
+        const int pair = col == kNoColumn ? none : (int)(col & 0xFFFFu);
+        const uint4 *src = reinterpret_cast<const uint4 *>(ws.act + (int64_t)pair * I + kb * SB + 16 * t);
+        const uint8_t *ex = ws.act_exp + (int64_t)pair * (I >> 4) + 8 * kb + t;
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-            o.v[c][0] = some ? __ldcg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-            o.v[c][1] = some ? __ldcg(src + 8 * c + 1) : make_uint4(0u, 0u, 0u, 0u);
-            o.ex[c] = some ? __ldcg(ex + 4 * c) : -1;
+            o.v[c][0] = __ldcg(src + 8 * c);
+            o.v[c][1] = __ldcg(src + 8 * c + 1);
+            o.ex[c] = __ldcg(ex + 4 * c);
         }
         // the tile's rows lie in one scale block
-        o.sc = in ? __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * kTile / 128) * ib + kb) : 0.0f;
+        o.sc = __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * kTile / 128) * ib + kb);
     };
     // act brought to its row's power of two: a factor of 2^-d, exact down to
     // FP16's subnormals
     auto to_row = [&](const uint4(&v)[2], int ex, int row_exp, uint32_t(&o)[8]) {
-        const int d = ex < 0 ? 25 : exp_shift(ex) - row_exp;  // >= 0
-        const __half f = d > 24 ? __ushort_as_half((unsigned short)0)
-                                : (d <= 14 ? __ushort_as_half((unsigned short)((15 - d) << 10))
-                                           : __ushort_as_half((unsigned short)(1 << (24 - d))));
+        const int d = min(exp_shift(ex) - row_exp, 40);  // >= 0
+        const __half f = __float2half_rn(__uint_as_float((uint32_t)(127 - d) << 23));  // 2^-d, 0 from 2^-25 on
         const __half2 f2 = __half2half2(f);
         const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
@@ -793,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto step = [&](Input &in, int u) {
         const uint32_t col = R->column[cur.ai][g];
-        const int row_exp = col == kNoColumn ? 0 : shift[col & 0xFFFFu];
+        const int row_exp = shift[col == kNoColumn ? none : (int)(col & 0xFFFFu)];
         uint32_t f[2][8];
 #pragma unroll
         for (int c = 0; c < 2; c++) to_row(in.v[c], in.ex[c], row_exp, f[c]);
@@ -850,7 +863,7 @@ Ring ring_for(int k) {
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
-    const size_t pairs = (size_t)tokens * topk;
+    const size_t pairs = (size_t)tokens * topk + 1;
     const size_t act = align256(pairs * inter * sizeof(__half)), ex = align256(pairs * (inter / 16)),
                  count = align256((size_t)hidden / kTile * sizeof(int)),
                  part = (size_t)sm_count() * 2 * kPart * sizeof(float);
