@@ -91,6 +91,18 @@ struct Ring {
 __device__ __forceinline__ void consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
 }
+// 32 bytes (32-byte aligned) through L2 where p holds, else zeros; no branch.
+__device__ __forceinline__ void ld_32b_if(bool p, const void *src, uint32_t (&v)[8]) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %9, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "mov.b32 %4, 0;\n\tmov.b32 %5, 0;\n\tmov.b32 %6, 0;\n\tmov.b32 %7, 0;\n\t"
+        "@p ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t}"
+        : "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]), "=&r"(v[5]), "=&r"(v[6]), "=&r"(v[7])
+        : "l"(src), "r"((int)p)
+        : "memory");
+}
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- routing --
@@ -383,8 +395,8 @@ __device__ __forceinline__ int token_of(uint32_t column) { return column == kNoC
 
 // Workspace layout.
 struct Ws {
-    __half *act;       // [tokens * topk + 1, inter], times a power of two per 16; the last row is zeros
-    uint8_t *act_exp;  // [tokens * topk + 1, inter / 16]: exponent field of the 16 values' largest
+    __half *act;       // [tokens * topk, inter], times a power of two per 16
+    uint8_t *act_exp;  // [tokens * topk, inter / 16]: exponent field of the 16 values' largest
     int *count;        // [hidden / kTile] shares of a tile that have come
     float *part;       // [CTAs][2][kPart] FP32 sums of shared tiles
 };
@@ -511,11 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.topk_weights) a.topk_weights[t * a.topk + j] = R->weight[t][j];
         }
         for (int i = threadIdx.x; i < H / kTile; i += 32 * kConsumers) ws.count[i] = 0;
-        // the row of zeros that columns without a token read
-        const int64_t none = (int64_t)T * a.topk;
-        for (int i = threadIdx.x; i < (I >> 3); i += 32 * kConsumers)
-            reinterpret_cast<uint4 *>(ws.act + none * I)[i] = make_uint4(0u, 0u, 0u, 0u);
-        for (int i = threadIdx.x; i < (I >> 4); i += 32 * kConsumers) ws.act_exp[none * (I >> 4) + i] = 0;
     }
 
     consumers_sync();
@@ -652,10 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     // every (token, choice)'s power of two, from its groups' exponents
-    const int none = T * a.topk;  // the row of zeros
-    if (threadIdx.x == 0) shift[none] = 0;
+    const int pairs = T * a.topk;
     constexpr int PB = 4;  // pairs of a warp whose loads are in flight together
-    for (int p0 = warp; p0 < none; p0 += PB * kConsumers) {
+    for (int p0 = warp; p0 < pairs; p0 += PB * kConsumers) {
         uint32_t mx[PB];
 #pragma unroll
         for (int i = 0; i < PB; i++) mx[i] = 0;
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint2 v[PB];
 #pragma unroll
             for (int i = 0; i < PB; i++) {
-                const int p = min(p0 + i * kConsumers, none - 1);
+                const int p = min(p0 + i * kConsumers, pairs - 1);
                 v[i] = __ldcg(reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)p * (I >> 4)) + k);
             }
 #pragma unroll
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[i] = __vmaxu4(mx[i], mx[i] >> 16);
             mx[i] = __reduce_max_sync(0xFFFFFFFFu, max(mx[i] & 0xFFu, (mx[i] >> 8) & 0xFFu));
             // (a pair of weight 0 has no act, and no column refers to it)
-            if (lane == 0 && p < none) {
+            if (lane == 0 && p < pairs) {
                 const int s = exp_shift((int)mx[i]);
                 shift[p] = (int8_t)s;
                 coef[p] = R->weight[p / a.topk][p % a.topk] * pow2i(-s);
@@ -687,11 +693,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7, ib = I >> 7;
-    // A step's input of this lane: its token's act, 2 x 16 FP16 values, their
-    // groups' exponents, and the scale of this warp's block.
+    // A step's input of this lane: its token's act, 2 x 16 FP16 values, the
+    // exponents of the block's eight groups, and the block's weight scale.
     struct Input {
-        uint4 v[2][2];
-        int ex[2];
+        uint32_t v[2][8];
+        uint2 ex;
         float sc;
     };
     // a place in the sequence
@@ -711,28 +717,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (past the end of K some other valid values, not used; no branch)
         const int kb = min(p.q * ring.blocks + warp, ib - 1);
         const uint32_t col = R->column[p.ai][g];
-        const int pair = col == kNoColumn ? none : (int)(col & 0xFFFFu);
-        const uint4 *src = reinterpret_cast<const uint4 *>(ws.act + (int64_t)pair * I + kb * SB + 16 * t);
-        const uint8_t *ex = ws.act_exp + (int64_t)pair * (I >> 4) + 8 * kb + t;
+        const int pair = col == kNoColumn ? 0 : (int)(col & 0xFFFFu);
+        const __half *src = ws.act + (int64_t)pair * I + kb * SB + 16 * t;
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-            o.v[c][0] = __ldcg(src + 8 * c);
-            o.v[c][1] = __ldcg(src + 8 * c + 1);
-            o.ex[c] = __ldcg(ex + 4 * c);
-        }
+        for (int c = 0; c < 2; c++) ld_32b_if(col != kNoColumn, src + CH * c, o.v[c]);
+        o.ex = __ldcg(reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)pair * (I >> 4)) + kb);
         // the tile's rows lie in one scale block
         o.sc = __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * kTile / 128) * ib + kb);
     };
     // act brought to its row's power of two: a factor of 2^-d, exact down to
     // FP16's subnormals
-    auto to_row = [&](const uint4(&v)[2], int ex, int row_exp, uint32_t(&o)[8]) {
-        const int d = min(exp_shift(ex) - row_exp, 40);  // >= 0
+    auto to_row = [&](const uint32_t(&v)[8], uint32_t exps, int row_exp, uint32_t(&o)[8]) {
+        const int d = min(max(exp_shift((int)((exps >> (8 * t)) & 0xFFu)) - row_exp, 0), 40);
         const __half f = __float2half_rn(__uint_as_float((uint32_t)(127 - d) << 23));  // 2^-d, 0 from 2^-25 on
         const __half2 f2 = __half2half2(f);
-        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&w[j]), f2);
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&v[j]), f2);
             o[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
     };
@@ -753,12 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int first = st;  // the tile's first step here
     float acc[kTile / 16][4] = {};
     clear();
-    // two steps ahead: one lasts about as long as the way to L2 and back
-    Input in0, in1;
+    Input in;  // one step ahead
     ahead = cur;
-    if (u_begin < u_end) load(ahead, in0);
-    advance(ahead);
-    if (u_begin + 1 < u_end) load(ahead, in1);
+    if (u_begin < u_end) load(ahead, in);
     advance(ahead);
     // The tile's sums over the warps, in warp order.  A tile shared with other
     // CTAs: leave them in the workspace, count, and add everybody's if last.
@@ -804,14 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         consumers_sync();  // everybody's sums, and the flag, have been read
         clear();
     };
-    auto step = [&](Input &in, int u) {
+    auto step = [&](int u) {
         const uint32_t col = R->column[cur.ai][g];
-        const int row_exp = shift[col == kNoColumn ? none : (int)(col & 0xFFFFu)];
+        const int row_exp = col == kNoColumn ? 127 : shift[col & 0xFFFFu];  // (without a token: zeros)
         uint32_t f[2][8];
 #pragma unroll
-        for (int c = 0; c < 2; c++) to_row(in.v[c], in.ex[c], row_exp, f[c]);
+        for (int c = 0; c < 2; c++) to_row(in.v[c], c ? in.ex.y : in.ex.x, row_exp, f[c]);
         const float sc[2] = {in.sc, in.sc};
-        if (u + 2 < u_end) load(ahead, in);
+        if (u + 1 < u_end) load(ahead, in);
         advance(ahead);
         const bool active = warp < ring.blocks && cur.q * ring.blocks + warp < ib;
 #pragma unroll
@@ -838,10 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         finish_tile(tile, first != 0 || cur.tile == tile);
         first = 0;
     };
-    for (int u = u_begin; u < u_end; u += 2) {
-        step(in0, u);
-        if (u + 1 < u_end) step(in1, u + 1);
-    }
+    for (int u = u_begin; u < u_end; u++) step(u);
 }
 
 // -------------------------------------------------------------------- host --
@@ -863,18 +858,18 @@ Ring ring_for(int k) {
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
-    const size_t pairs = (size_t)tokens * topk + 1;
+    const size_t pairs = (size_t)tokens * topk;
     const size_t act = align256(pairs * inter * sizeof(__half)), ex = align256(pairs * (inter / 16)),
                  count = align256((size_t)hidden / kTile * sizeof(int)),
                  part = (size_t)sm_count() * 2 * kPart * sizeof(float);
     if (ws) {
-        uint8_t *b = static_cast<uint8_t *>(p);
+        uint8_t *b = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 255) & ~uintptr_t(255));
         ws->act = reinterpret_cast<__half *>(b);
         ws->act_exp = b + act;
         ws->count = reinterpret_cast<int *>(b + act + ex);
         ws->part = reinterpret_cast<float *>(b + act + ex + count);
     }
-    return act + ex + count + part;
+    return 255 + act + ex + count + part;
 }
 
 template <class F>
