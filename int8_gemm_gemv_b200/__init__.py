@@ -44,6 +44,7 @@ class BsqError(RuntimeError):
 
 
 _lib = None
+_FUNCTIONS = {}  # by name, filled when the library is loaded
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -88,6 +89,7 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.argtypes = args
             f.restype = ctypes.c_int
+            _FUNCTIONS[name] = f
         L.bsq_status_string.argtypes = [ctypes.c_int]
         L.bsq_status_string.restype = ctypes.c_char_p
         L.bsq_debug_launch_count.argtypes = []
@@ -118,24 +120,74 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current = None  # torch's current device and raw current stream, looked up once
+
+
+def _torch_current():
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a fifth of the object's cost
+        if raw is None:
+            def raw(device):
+                return torch.cuda.current_stream(device).cuda_stream
+        _current = torch.cuda.current_device, raw
+    return _current
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        device, raw = _torch_current()
+        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
-def _call(name, *args):
+def _raise(name, st):
     L = lib()
-    st = getattr(L, name)(*args)
+    detail = None
+    if st == BSQ_ERR_CUDA:
+        code = L.bsq_debug_take_cuda_error()
+        detail = f"cudaError {code}: {L.bsq_debug_cuda_error_string(code).decode()}"
+    raise BsqError(st, name, detail)
+
+
+def _call(name, *args):
+    st = getattr(lib(), name)(*args)
     if st != BSQ_OK:
-        detail = None
-        if st == BSQ_ERR_CUDA:
-            code = L.bsq_debug_take_cuda_error()
-            detail = f"cudaError {code}: {L.bsq_debug_cuda_error_string(code).decode()}"
-        raise BsqError(st, name, detail)
+        _raise(name, st)
+
+
+def _on_device(tensors):
+    """The addresses of tensors, which must lie on the current device (None and
+    raw addresses are passed on)."""
+    args = []
+    device = None
+    for t in tensors:
+        if t is None or type(t) is int:
+            args.append(t)
+            continue
+        on = t.get_device()
+        if on != device:
+            if on < 0:
+                raise ValueError("libbsq takes CUDA tensors (device memory)")
+            device = _torch_current()[0]()
+            if on != device:
+                raise ValueError(f"libbsq takes tensors on the current device (cuda:{device}), got cuda:{on}")
+        if not t.is_contiguous():
+            raise ValueError("libbsq takes contiguous tensors")
+        args.append(t.data_ptr())
+    return args
+
+
+def _launch(name, *args):
+    if _lib is None:
+        lib()
+    st = _FUNCTIONS[name](*args)
+    if st != BSQ_OK:
+        _raise(name, st)
 
 
 def status_string(status: int) -> str:
@@ -240,22 +292,21 @@ def fp8_gemm_rowscale(a, a_scale, w, w_scale, out, m, n, k, stream=None):
 
 def rmsnorm_residual_quant_fp8(x, residual, gain, eps, residual_out, q, scale, group, m, k, stream=None):
     """residual and residual_out may be None; group 128 (scale [m, k/128]) or 0 (one scale per row)."""
-    _call("rmsnorm_residual_quant_fp8", _ptr(x), _ptr(residual), _ptr(gain), eps, _ptr(residual_out), _ptr(q),
-          _ptr(scale), group, m, k, _stream(stream))
+    x, residual, gain, residual_out, q, scale = _on_device((x, residual, gain, residual_out, q, scale))
+    _launch("rmsnorm_residual_quant_fp8", x, residual, gain, eps, residual_out, q, scale, group, m, k, _stream(stream))
 
 
 def quant_act_fp8_per128(a, a_fp8, a_scale, m, k, stream=None):
-    _call("quant_act_fp8_per128", _ptr(a), _ptr(a_fp8), _ptr(a_scale), m, k, _stream(stream))
+    _launch("quant_act_fp8_per128", *_on_device((a, a_fp8, a_scale)), m, k, _stream(stream))
 
 
 def silu_mul_quant_fp8_per128(gate_up, a_fp8, a_scale, m, k, stream=None):
     """gate_up [m, 2k]: the gate's k columns, then the up projection's."""
-    _call("silu_mul_quant_fp8_per128", _ptr(gate_up), _ptr(a_fp8), _ptr(a_scale), m, k, _stream(stream))
+    _launch("silu_mul_quant_fp8_per128", *_on_device((gate_up, a_fp8, a_scale)), m, k, _stream(stream))
 
 
 def fp8_gemm_blockscaled(a, a_scale, w, w_scale, out, m, n, k, stream=None):
-    _call("fp8_gemm_blockscaled", _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(out), m, n, k,
-          _stream(stream))
+    _launch("fp8_gemm_blockscaled", *_on_device((a, a_scale, w, w_scale, out)), m, n, k, _stream(stream))
 
 
 def fp8_moe_workspace_bytes(tokens, hidden, inter, topk):
@@ -267,9 +318,10 @@ def fp8_moe_workspace_bytes(tokens, hidden, inter, topk):
 def fp8_moe_blockscaled(x, logits, w_gate_up, gate_up_scale, w_down, down_scale, out, topk_ids, topk_weights,
                         workspace, ws_bytes, tokens, hidden, inter, experts, topk, renormalise, stream=None):
     """topk_ids and topk_weights may be None; see include/bsq.h."""
-    _call("fp8_moe_blockscaled", _ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(gate_up_scale), _ptr(w_down),
-          _ptr(down_scale), _ptr(out), _ptr(topk_ids), _ptr(topk_weights), _ptr(workspace), ws_bytes, tokens, hidden,
-          inter, experts, topk, int(renormalise), _stream(stream))
+    pointers = _on_device((x, logits, w_gate_up, gate_up_scale, w_down, down_scale, out, topk_ids, topk_weights,
+                           workspace))
+    _launch("fp8_moe_blockscaled", *pointers, ws_bytes, tokens, hidden, inter, experts, topk, int(renormalise),
+            _stream(stream))
 
 
 def bsq_amax_bf16(x, count, amax_dev, stream=None):
