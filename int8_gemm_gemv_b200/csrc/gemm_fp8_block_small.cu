@@ -337,42 +337,95 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
+constexpr size_t kWholeSm = 226 * 1024, kHalfSm = 112 * 1024;
+
+template <int NT> int ring_stages(size_t room) {
+    const int n = (int)((room - 1024 - sizeof(Smem<NT>)) / Cfg<NT>::STAGE_BYTES);
+    return n < kMaxStages ? n : kMaxStages;
+}
+
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Launch(int split, int tiles_n, int tiles_m, size_t smem, cudaStream_t s) {
+        cfg.gridDim = dim3(split * tiles_n, tiles_m);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+// Clusters of `split` CTAs that can be resident at once (cached per device).
+// Two CTAs share an SM here (half of its shared memory, a third of its
+// registers and at most 128 of its 512 tensor-memory columns each), but the
+// occupancy query counts one per SM for a kernel that allocates tensor memory,
+// whatever its size, so its answer is doubled: the step in the measured times
+// comes there (40 tiles: 6 x 40 CTAs 9.0 us, 7 x 40 14.0; 80 tiles of 64 x
+// 5120 x 17408: 3 x 80 23 us, 4 x 80 35).
+template <int NT> int max_clusters(int split) {
+    // a racing first call computes the same value twice; the store is atomic
+    static std::atomic<int> cached[kMaxDevices][kMaxSplit + 1];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool cacheable = dev >= 0 && dev < kMaxDevices;
+    if (cacheable) {
+        const int c = cached[dev][split].load(std::memory_order_relaxed);
+        if (c > 0) return c;
+    }
+    Launch l(split, sm_count(), 1, smem_bytes<NT>(ring_stages<NT>(kHalfSm)), nullptr);
+    l.cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_gemm_small<NT>, &l.cfg) != cudaSuccess || n <= 0) n = 1;
+    n *= 2;
+    if (cacheable) cached[dev][split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs per tile: as many as can all be resident at once (a cluster too many
+// makes a second round, see above), but 1 where one CTA per tile nearly fills
+// the SMs already (17408 x 5120, 136 tiles: 17.4 us at 16 rows, 18.2 with two;
+// 17.5 and 19.5 at 32 rows) or where the ring holds
+// all of a tile's K anyway (64 x 5120 x 1408: 5.3 us, 7.1 with three), and
+// never below five K blocks each.
+template <int NT> int split_for(int64_t tiles, int nkb) {
+    if (4 * tiles >= 3 * (int64_t)sm_count() || nkb <= kMaxStages) return 1;
+    for (int split = nkb / 5 < kMaxSplit ? nkb / 5 : kMaxSplit; split > 1; split--)
+        if (tiles <= max_clusters<NT>(split)) return split;
+    return 1;
+}
+
 template <int NT>
 cudaError_t launch_nt(const uint8_t *a, const float *a_scale, const uint8_t *w, const float *w_scale, uint16_t *out,
-                      int m, int n, int k, int split, cudaStream_t s) {
+                      int m, int n, int k, cudaStream_t s) {
     alignas(64) CUtensorMap tW, tA;
     if (!make_tmap_2d(&tW, w, 1, k, n, k, BK, BW, true, false) || !make_tmap_2d(&tA, a, 1, k, m, k, BK, NT, true, false))
         return cudaErrorInvalidValue;
-    const int tiles_n = (n + BW - 1) / BW, tiles_m = (m + NT - 1) / NT;
-    const int64_t ctas = (int64_t)tiles_n * tiles_m * split;
-    // a whole SM's shared memory when every CTA has an SM to itself, half of
-    // it otherwise, and no more than the K blocks a CTA has
-    const size_t room = ctas <= sm_count() ? 226 * 1024 : 112 * 1024;
-    int stages = (int)((room - 1024 - sizeof(Smem<NT>)) / Cfg<NT>::STAGE_BYTES);
-    stages = stages < kMaxStages ? stages : kMaxStages;
-    // (the sums of a split tile need NT * 512 bytes of ring: at most two stages)
-    const int per_cta = (k / BK + split - 1) / split;
-    stages = stages < per_cta ? stages : (per_cta > 2 ? per_cta : 2);
     static DeviceOnce attrs;
     cudaError_t e = attrs.run([] {
-        return cudaFuncSetAttribute(k_gemm_small<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+        return cudaFuncSetAttribute(k_gemm_small<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWholeSm);
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split * tiles_n, tiles_m);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<NT>(stages);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_gemm_small<NT>, tW, tA, stages, a_scale, w_scale, out, m, n, k);
+    const int tiles_n = (n + BW - 1) / BW, tiles_m = (m + NT - 1) / NT, nkb = k / BK;
+    const int64_t tiles = (int64_t)tiles_n * tiles_m;
+    const int split = split_for<NT>(tiles, nkb);
+    // a whole SM's shared memory when every CTA has an SM to itself (clusters
+    // do not fill every SM: 17 tiles of 16 x 2112 x 17408, 8 x 17 CTAs, took
+    // 17.1 us with whole SMs, 10.5 with halves), half of it otherwise, and no
+    // more than the K blocks a CTA has
+    int stages = ring_stages<NT>(2 * tiles <= max_clusters<NT>(split) ? kWholeSm : kHalfSm);
+    // (the sums of a split tile need NT * 512 bytes of ring: at most two stages)
+    const int per_cta = (nkb + split - 1) / split;
+    stages = stages < per_cta ? stages : (per_cta > 2 ? per_cta : 2);
+    Launch l(split, tiles_n, tiles_m, smem_bytes<NT>(stages), s);
+    return cudaLaunchKernelEx(&l.cfg, k_gemm_small<NT>, tW, tA, stages, a_scale, w_scale, out, m, n, k);
 }
 
 static_assert(2 * Cfg<32>::STAGE_BYTES >= 32 * BW * 4 && 2 * Cfg<16>::STAGE_BYTES >= 16 * BW * 4, "sums in the ring");
@@ -388,26 +441,12 @@ uint32_t take_timeouts_gemm_fp8_block_small() {
 
 // Activation rows of a tile: 16 up to 16 rows, else 32 (tiles of 64 and 128
 // were slower at every size: the fold then needs more registers than two CTAs
-// per SM leave).  CTAs per tile: as many as bring the CTAs to two per SM, but
-// 1 where one CTA per tile nearly fills the SMs already (17408 x 5120 at 16
-// rows, 136 tiles: 17.1 us, 18.2 with two) or where the ring holds all of a
-// tile's K anyway (64 x 5120 x 1408: 5.3 us, 7.1 with three), and never below
-// five K blocks each (16 x 5120 x 5120: 9.0 us with three to six, 9.6 with
-// two; 16 x 1024 x 5120: 4.7 us with eight, 6.6 with three).
+// per SM leave).
 cudaError_t launch_fp8_gemm_blockscaled_small(const uint8_t *a, const float *a_scale, const uint8_t *w,
                                               const float *w_scale, uint16_t *out, int m, int n, int k,
                                               cudaStream_t s) {
-    const int nt = m <= 16 ? 16 : 32, nkb = k / BK;
-    const int64_t tiles = (int64_t)((n + BW - 1) / BW) * ((m + nt - 1) / nt);
-    int64_t split = 1;
-    if (4 * tiles < 3 * (int64_t)sm_count() && nkb > kMaxStages) {
-        split = 2 * (int64_t)sm_count() / tiles;
-        if (split > kMaxSplit) split = kMaxSplit;
-        if (split > nkb / 5) split = nkb / 5;
-        if (split < 1) split = 1;
-    }
-    return nt == 16 ? launch_nt<16>(a, a_scale, w, w_scale, out, m, n, k, (int)split, s)
-                    : launch_nt<32>(a, a_scale, w, w_scale, out, m, n, k, (int)split, s);
+    return m <= 16 ? launch_nt<16>(a, a_scale, w, w_scale, out, m, n, k, s)
+                   : launch_nt<32>(a, a_scale, w, w_scale, out, m, n, k, s);
 }
 
 }  // namespace bsq
