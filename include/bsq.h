@@ -397,8 +397,9 @@ BSQ_API bsq_status fp8_gemm_rowscale(const uint8_t *a, const float *a_scale,
  *   h = BF16_rne(x + residual) (FP32 sum; h = x without residual);
  *   y = (h * r) * gain, r = 1 / sqrt(sum h^2 / k + eps), all in FP32 and not
  *   rounded further; s = amax|y| / 448 over each group; q =
- *   E4M3_rne_satfinite(y / s); an all-zero group gives s = 0 and q = 0.  A
- *   row of zeros with eps = 0 gives zeros.
+ *   E4M3_rne_satfinite(y / s); an all-zero group gives s = 0 and q = 0.
+ *   sum h^2 must stay finite in FP32; a square below its range counts as 0,
+ *   and a row whose squares all do gives zeros where eps = 0.
  *   x, residual, gain, residual_out, q 16-byte aligned, scale 4-byte.
  * Errors: k % 16 != 0, group not 0 or 128, group 128 with k % 128 != 0, eps
  * negative or not finite -> INVALID_ARG; k > 65536 -> UNSUPPORTED.

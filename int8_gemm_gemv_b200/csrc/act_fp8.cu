@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
         __syncthreads();
         ss = warp_sum(lane < (nt >> 5) ? red[0][lane] : 0.0f);
     }
-    const float r = rsqrtf(__fdiv_rn(ss, (float)k) + eps);
+    const float mean = __fdiv_rn(ss, (float)k) + eps;
     // (a row of zeros without eps: zeros, not 0 * inf)
-    const float f = ss > 0.0f ? r : 0.0f;
+    const float f = mean == 0.0f ? 0.0f : rsqrtf(mean);
     auto normed = [&](int i, float(&y)[16]) {
         const int u = tid + i * nt;
         const Unit g = u < units ? ld_unit(gain + 16 * u) : zero_unit();

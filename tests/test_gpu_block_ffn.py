@@ -177,6 +177,51 @@ def test_rmsnorm_zero_row_without_eps():
     check_codes(q[1:], s[1:], norm_exact(x[1:], gain, 0.0), 128, norm_rel(256), "one spike")
 
 
+@pytest.mark.parametrize("group", [128, 0])
+def test_rmsnorm_rows_whose_squares_vanish(group):
+    """eps alone under the root: h^2 is below FP32's range, h and y are not."""
+    x = (activations(3, 1024, 9).float() * 1e-25).bfloat16()
+    gain = torch.ones(1024, dtype=torch.bfloat16, device=DEV)
+    q, s = poisoned((3, 1024), torch.uint8), poisoned((3, 8) if group else (3,), torch.float32)
+    bsq.rmsnorm_residual_quant_fp8(x, None, gain, 1e-6, None, q, s, group, 3, 1024)
+    check_codes(q, s, norm_exact(x, gain, 1e-6), group, norm_rel(1024), group)
+
+
+# ------------------------------------------------- offsets past 32 bits ---
+
+def test_rows_past_two_to_the_31_elements():
+    """A row's result does not depend on where it lies."""
+    m, k, last = 131200, 16384, 3
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device=DEV)
+    assert x.numel() > 2**31
+    x[-last:] = activations(last, k, 10)
+    gain = activations(1, k, 11)[0]
+    for groups, call in ((k // 128, lambda x, q, s, m: bsq.quant_act_fp8_per128(x, q, s, m, k)),
+                         (1, lambda x, q, s, m: bsq.rmsnorm_residual_quant_fp8(x, None, gain, 1e-6, None, q, s, 0, m,
+                                                                               k)),
+                         (k // 256, lambda x, q, s, m: bsq.silu_mul_quant_fp8_per128(x, q, s, m, k // 2))):
+        width = k // 2 if groups == k // 256 else k
+        q, s = poisoned((m, width), torch.uint8), poisoned((m, groups), torch.float32)
+        call(x, q, s, m)
+        q1, s1 = poisoned((last, width), torch.uint8), poisoned((last, groups), torch.float32)
+        call(x[-last:], q1, s1, last)
+        assert torch.equal(q[-last:], q1) and torch.equal(s[-last:], s1)
+        assert not (q[:-last].any() or s[:-last].any())
+
+
+@pytest.mark.parametrize("n", [16400, 16401])
+def test_gemm_output_past_two_to_the_31_elements(n):
+    m, k, last = 131200, 256, 3
+    a, sa = torch.zeros(m, k, dtype=torch.uint8, device=DEV), scales((m, k // 128), 12)
+    a[-last:] = codes((last, k), 13)
+    w, sw = codes((n, k), 14), scales(((n + 127) // 128, k // 128), 15)
+    out = poisoned((m, n), torch.bfloat16)
+    assert out.numel() > 2**31
+    bsq.fp8_gemm_blockscaled(a, sa, w, sw, out, m, n, k)
+    check_gemm(out[-last:], a[-last:], sa[-last:], w, sw, n)
+    assert not out[:-last].any()
+
+
 # ---------------------------------------------------------------- GEMM ---
 
 def dequant_a(a, sa):
@@ -387,6 +432,26 @@ def test_moe_wide_activation_range():
     m.x[2, ::2] *= 2.0**-20
     m()
     m.check()
+
+
+def test_moe_weights_past_two_to_the_32_bytes():
+    """The last experts of a large layer give what they give in a small one."""
+    t, h, i, e, topk = 3, 2048, 2048, 512, 2
+    small = Moe(t, h, i, 2, topk, 1, seed=21)
+    small()
+    small.check()
+    w13 = torch.zeros(e, 2 * i, h, dtype=torch.uint8, device=DEV)
+    w2 = torch.zeros(e, h, i, dtype=torch.uint8, device=DEV)
+    assert w13.numel() > 2**32 - 1
+    s13, s2 = torch.ones(e, 2 * i // 128, h // 128, device=DEV), torch.ones(e, h // 128, i // 128, device=DEV)
+    logits = torch.full((t, e), -torch.inf, device=DEV)
+    for to, of in ((w13, small.w13), (w2, small.w2), (s13, small.s13), (s2, small.s2)):
+        to[-2:] = of
+    logits[:, -2:] = small.logits
+    out, ids = poisoned((t, h), torch.bfloat16), poisoned((t, topk), torch.int32)
+    bsq.fp8_moe_blockscaled(small.x, logits, w13, s13, w2, s2, out, ids, None, small.ws, small.bytes, t, h, i, e, topk,
+                            1)
+    assert torch.equal(out, small.out[:t]) and torch.equal(ids, small.ids + e - 2)
 
 
 def test_moe_ids_may_be_null():
