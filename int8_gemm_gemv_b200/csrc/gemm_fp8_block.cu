@@ -4,34 +4,37 @@
 //
 // The tensor cores sum one block of 128 at a time into tensor memory; the
 // FP32 lanes fold each block with its scales into accumulators that stay in
-// registers.  In a 256-column tile a thread holds one output row and 128
-// columns, all inside one 128-wide scale block, so a block's two scales
-// multiply to one factor per thread and the fold is one FMA per output.
+// registers.  An output tile is one weight scale block wide, so a block's two
+// scales multiply to one factor per row and the fold is one FMA per output.
 //
-// CTA pairs (clusters of two SMs), persistent over 256 x 256 output tiles.
-// One pair MMA (tcgen05.mma.cta_group::2, 256 x 256 x 32) runs on both SMs'
-// tensor cores; each CTA holds 128 rows of A and 128 of the tile's 256 weight
-// rows and receives 128 x 256 of the products in its tensor memory.
+// CTA pairs (clusters of two SMs), persistent over 256 x 128 output tiles.
+// One pair MMA (tcgen05.mma.cta_group::2, 256 x 128 x 32) runs on both SMs'
+// tensor cores; each CTA holds 128 rows of A and 64 of the tile's 128 weight
+// rows and receives 128 x 128 of the products in its tensor memory.
 // Per CTA (384 threads):
-//   warp 0      TMA producer, a six-stage ring of one K block each (16 KB of
-//               A, 16 KB of W), counted on the even CTA's barrier
-//   warp 1      tensor memory for the pair; in the even CTA, one thread
-//               issues the MMAs: per block and column half four of 256 x 128
-//               x 32 into one of that half's two 128-column buffers
+//   warp 0      TMA producer, a ring of STAGES stages of GB = 2 K blocks (32
+//               KB of A, 16 KB of W), counted on the even CTA's barrier
+//   warp 1      tensor memory for the pair; in the even CTA, one elected
+//               thread issues the MMAs: per stage two blocks of four 256 x 128
+//               x 32 into one of NBUF = 2 buffers (of two 128-column blocks:
+//               all 512 columns)
 //   warp 2      brings the activation and weight scales into shared memory,
 //               four blocks at a time (one load per activation row and fold
 //               thread, straight from global memory, cost more than the MMAs)
-//   warps 4..11 fold and epilogue: warp w owns lane group w % 4 and column
-//               half (w - 4) / 4; output through swizzled shared memory and
-//               TMA stores (plain stores where a row is not a multiple of 16
-//               bytes)
-// Per SM and K block the MMAs take 512 cycles and the fold's 32,768 FMAs 256
-// of the FP32 lanes' cycles.  A buffer goes round MMA (256 cycles), commit
-// (about 170), fold (about 450) and the arrival at the even CTA (about 150):
-// four buffers of 128 columns cover that, two of 256 columns (with 512 cycles
-// of MMA in the round) did not.  128 columns run at the tensor cores' full
-// rate as long as the issue takes less than 64 cycles per MMA, hence the
-// precomputed descriptors.
+//   warps 4..11 fold and epilogue: warp w owns lane group w % 4 (32 rows) and
+//               64 columns, (w - 4) / 4; output through swizzled shared memory
+//               and TMA stores (plain stores where a row is not a multiple of
+//               16 bytes)
+// Per SM and K block the MMAs take 256 cycles and the fold's 16,384 FMAs 64 to
+// 128 of the FP32 lanes' cycles; a block takes about 420.  What is between is
+// the round of a buffer: MMAs, commit, the waiting warps' wake-up, two
+// tensor-memory loads of 64 columns, the arrival at the even CTA.  Two blocks
+// per stage halve the rounds, and the issue takes about 50 cycles per MMA
+// (elected thread, precomputed descriptor words), under the 64 that it runs.
+// 4096 x 17408 x 5120: 340 to 400 us by operands' values (1.83 to 2.15
+// PFLOP/s; the power limit acts), 225 at twice the BF16 rate of a plain
+// product.  Tiles of 256 x 256 (fold of 128 registers per thread, 16 or 8
+// warps), one block per stage, and two tiles in turn were not faster.
 //
 // Launched with programmatic stream serialization: every role waits for the
 // previous kernel (griddepcontrol.wait) before its first global access.
@@ -139,7 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int num_tiles = tiles_m * tiles_n;
     const int nkb = K / BK, ngr = (nkb + GB - 1) / GB;
 
-    launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
             mbar_init(&S->full[s], 1);
@@ -165,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
+    launch_dependents();  // only now: a dependent must not take the tensor memory first
+    dependency_wait();    // every role: the bounded waits start with this kernel's own work
     const uint32_t tmem = S->tmem_base;
     auto leader = [&](uint64_t *bar) { return mapa_shared(smem_u32(bar), 0); };
 
@@ -174,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tensormap(&tmA);
             prefetch_tensormap(&tmB);
             const uint32_t full0 = leader(&S->full[0]);
-            dependency_wait();
             uint32_t it = 0, ph = 1;
             int s = 0;
             bool ok = true, ready = mbar_test(&S->empty[0], 1);
@@ -252,7 +255,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 2) {
         // ------------------------------------------------------- scales
-        dependency_wait();
         const bool vec = (nkb & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(a_scale) | reinterpret_cast<uintptr_t>(w_scale)) & 15) == 0;
         uint32_t g = 0;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // arrivals through the cluster address even where the barrier is this
         // CTA's: the plain form takes 160 cycles here, this one none
         const uint32_t sempty0 = mapa_shared(smem_u32(&S->sempty[0]), rank);
-        if (lane == 0) prefetch_tensormap(&tmOut);
+        if (use_tma_store && lane == 0) prefetch_tensormap(&tmOut);
         uint32_t bph = 0, sph = 0;
         int b = 0, ss = 0;
         bool ready = false;

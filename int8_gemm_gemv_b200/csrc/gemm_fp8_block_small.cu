@@ -120,7 +120,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kb0 = (int)((int64_t)nkb_all * rank / split), nkb = (int)((int64_t)nkb_all * (rank + 1) / split) - kb0;
     const int n0 = (int)(blockIdx.x / split) * BW, m0 = (int)blockIdx.y * NT;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) {
             mbar_init(&S->full[s], 1);
@@ -145,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // only now: a dependent must not take the tensor memory first
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = S->tmem_base;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 

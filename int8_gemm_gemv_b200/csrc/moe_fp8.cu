@@ -9,8 +9,8 @@
 // warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, two
 // boxes to a slot, and eight consumer warps that split a box's K into its
 // 128-wide scale blocks (E4M3 -> FP16 exactly, FP16 MMAs with FP32 sums, each
-// block's sum times its scale).  The MMA's eight columns are tokens: those that chose the expert
-// (gate, up), or all of them with zeros where they did not (down).
+// block's sum times its scale).  The MMA's eight columns are tokens that chose
+// the expert (more than eight: it is listed, and read, twice).
 //
 //   k_moe_gate_up  every CTA routes all tokens by itself (some hundred
 //                  instructions per token), then takes an equal share of the
@@ -21,8 +21,8 @@
 //   k_moe_down     an output tile of 64 rows runs over all reached experts'
 //                  K, so a token's experts add up in registers.  The (tile,
 //                  expert, K) steps are cut into equal shares, one per CTA,
-//                  also inside a tile: 448 tiles on 148 SMs would otherwise
-//                  leave a quarter of them idle.  CTAs that share a tile leave
+//                  also inside a tile: the 80 tiles of 5120 outputs alone
+//                  would occupy 80 of 148 SMs.  CTAs that share a tile leave
 //                  their FP32 sums in the workspace, and the last one to come
 //                  adds them in share order, so the result does not depend on
 //                  which was last.  No CTA waits for another.
@@ -43,8 +43,8 @@ namespace {
 using namespace gv;
 
 // Eight consumer warps, so that each has the registers to run a slot's boxes
-// as independent chains of MMAs (sixteen warps of half the work took 600
-// cycles per box, more than the 700 that the stream leaves for two).
+// as independent chains of MMAs (sixteen warps, one scale block of one box
+// each, were slower).
 constexpr int kConsumers = 8;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int SB = 128;        // K of one scale block: two 64-byte chunks
