@@ -52,8 +52,11 @@ constexpr int kMaxSlots = 16;
 constexpr int kMaxActive = kMoeMaxTokens * kMoeMaxTopk;
 constexpr int kRed = 8704;     // floats of the warps' partial sums; the routing keys before that
 constexpr int kSums = 512;     // floats of a group's sums: tiles x 16 rows x 8 columns
-constexpr int kTile = 64;      // rows of an output tile: two slots per step
-constexpr int kPart = kTile * kMoeMaxTokens;  // floats of an output tile's sums
+// Down kernel: a warp sums kOwn rows of an output tile; the tile's rows follow
+// from how many scale blocks of K the warps take side by side.
+constexpr int kOwn = 64;
+constexpr int tile_rows(int wide) { return kOwn * kConsumers / wide; }
+constexpr int kMinTile = tile_rows(8), kMaxTile = tile_rows(4);
 static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums && 2 * kMaxActive <= kSums && kMaxActive + 1 <= 4 * (kSums - kMaxActive),
               "shared buffers");
 
@@ -82,10 +85,12 @@ struct alignas(16) Bars {
     uint32_t last;  // this CTA finishes the tile
 };
 
-// Ring geometry: a slot holds two boxes of 16 weight rows x `blocks` scale
-// blocks of K; `steps` slots along K, `slots` in the ring.
+// Ring geometry: a slot holds boxes of 16 weight rows x `blocks` scale blocks
+// of K (box_bytes each), as many as the kernel has per step or pair; `steps`
+// along K, `slots` in the ring.
 struct Ring {
     int blocks, steps, slots;
+    __host__ __device__ int box_bytes() const { return blocks * 16 * SB; }
 };
 
 __device__ __forceinline__ void consumers_sync() {
@@ -299,13 +304,13 @@ __device__ __forceinline__ void chunk_mma_8(float (&d)[4], const uint4 &wa, cons
     }
 }
 
-// The next slot: acc[box] += scale[box] * (this warp's scale block, two chunks,
-// of the slot's box) x the activation fragments x[chunk], as four independent
-// chains of MMAs.
-__device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, int slot_bytes, int slots, bool active,
-                                         int warp, int lane, const uint32_t (&x)[2][8], const float (&scale)[2],
-                                         float (&acc0)[4], float (&acc1)[4]) {
-    const uint32_t at = take.take(S, ring, slot_bytes) + warp * 2 * 16 * CH;
+// Two boxes of the next slot: acc[box] += scale[box] * (this warp's scale
+// block, two chunks, of the box) x the activation fragments x[chunk], as four
+// independent chains of MMAs.  `offset` is that block's place in the slot.
+__device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, int slot_bytes, int slots, int box_bytes,
+                                         int offset, bool active, int lane, const uint32_t (&x)[2][8],
+                                         const float (&scale)[2], float (&acc0)[4], float (&acc1)[4]) {
+    const uint32_t at = take.take(S, ring, slot_bytes) + offset;
     const int g = lane >> 2, t = lane & 3;
     uint4 w[2][2][2];  // [box][chunk][row g, g + 8]
     if (active) {
@@ -313,7 +318,7 @@ __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, in
         for (int v = 0; v < 2; v++)
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                const uint32_t chunk = at + v * (slot_bytes >> 1) + c * 16 * CH;
+                const uint32_t chunk = at + v * box_bytes + c * 16 * CH;
                 w[v][c][0] = lds_v4(chunk + w_off(g, t));
                 w[v][c][1] = lds_v4(chunk + w_off(g + 8, t));
             }
@@ -337,12 +342,16 @@ struct Giver {
     int s = 0;
     uint32_t ph = 1;
     uint32_t it = 0;
-    __device__ __forceinline__ bool give(Bars *S, uint8_t *ring, int slot_bytes, int slots, const CUtensorMap *tm,
-                                         int row0, int row1, int chunk) {
+    // BOXES boxes, box b at weight row row0 + b * apart
+    template <int BOXES>
+    __device__ __forceinline__ bool give(Bars *S, uint8_t *ring, int box_bytes, int slots, const CUtensorMap *tm,
+                                         int row0, int apart, int chunk) {
+        const int slot_bytes = BOXES * box_bytes;
         if (!mbar_wait(&S->empty[s], ph, &g_timeouts) || *(volatile uint32_t *)&S->abort) return false;
         mbar_arrive_expect_tx(&S->full[s], slot_bytes);
-        tma_load_3d(ring + (size_t)s * slot_bytes, tm, &S->full[s], 0, row0, chunk);
-        tma_load_3d(ring + (size_t)s * slot_bytes + (slot_bytes >> 1), tm, &S->full[s], 0, row1, chunk);
+#pragma unroll
+        for (int b = 0; b < BOXES; b++)
+            tma_load_3d(ring + (size_t)s * slot_bytes + b * box_bytes, tm, &S->full[s], 0, row0 + b * apart, chunk);
         if (++s == slots) {
             s = 0;
             ph ^= 1;
@@ -412,8 +421,8 @@ __device__ __forceinline__ int token_of(uint32_t column) { return column == kNoC
 struct Ws {
     __half *act;       // [tokens * topk, inter], times a power of two per 16
     uint8_t *act_exp;  // [tokens * topk, inter / 16]: exponent field of the 16 values' largest
-    int *count;        // [hidden / kTile] shares of a tile that have come
-    float *part;       // [CTAs][2][kPart] FP32 sums of shared tiles
+    int *count;        // [output tiles] shares of a tile that have come
+    float *part;       // [CTAs][2][tile rows x tokens] FP32 sums of shared tiles
 };
 
 // The power of two for 16 (or a row of) act values whose largest has this
@@ -425,10 +434,10 @@ __device__ __forceinline__ int exp_shift(int e) { return min(14 - (e - 127), 127
 //        (64, 16, 2 ring.blocks)
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_gate_up(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
-    constexpr int PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x
+    constexpr int PG = 2, TG = 2 * PG;  // (gate, up) tile pairs sharing one pass over x; a slot holds one pair
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int slot_bytes = 2 * ring.blocks * 16 * SB;
+    const int box_bytes = ring.box_bytes(), slot_bytes = 2 * box_bytes;
     float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
     float *sums = red + kRed;
     Route *R = reinterpret_cast<Route *>(sums + kSums);
@@ -461,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row = (int)R->expert[ai] * 2 * I + 16 * r;
                 for (int q = 0; q < ring.steps && ok; q++)
                     for (int p = 0; p < n && ok; p++)
-                        ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 16 * p, row + 16 * p + I,
-                                       q * ring.blocks * 2);
+                        ok = give.give<2>(S, base, box_bytes, ring.slots, &tmW, row + 16 * p, I, q * ring.blocks * 2);
                 u += n;
             }
             if (!ok) give.give_up(S, ring.slots);
@@ -537,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.topk_ids) a.topk_ids[t * a.topk + j] = R->id[t][j];
             if (a.topk_weights) a.topk_weights[t * a.topk + j] = R->weight[t][j];
         }
-        for (int i = threadIdx.x; i < H / kTile; i += 32 * kConsumers) ws.count[i] = 0;
+        for (int i = threadIdx.x; i < H / kMinTile; i += 32 * kConsumers) ws.count[i] = 0;
     }
 
     consumers_sync();
@@ -567,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < PG; p++) {
                 if (p >= n) break;
-                slot_mma(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, sc[p], acc[2 * p],
-                         acc[2 * p + 1]);
+                slot_mma(take, S, ring_at, slot_bytes, ring.slots, box_bytes, warp * 2 * 16 * CH, active, lane, f, sc[p],
+                         acc[2 * p], acc[2 * p + 1]);
             }
         }
         reduce_warps<TG>(acc, red, sums, warp, lane, 2 * n * 128);
@@ -609,14 +617,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 // -------------------------------------------------------------------- down --
 //   tmW  [experts * hidden] rows x inter, as (64 B, rows, inter / 64), box
 //        (64, 16, 2 ring.blocks)
+// The eight warps take WIDE scale blocks of K side by side, 8 / WIDE row halves
+// each: WIDE 8 and tiles of 64 rows, or WIDE 4 and tiles of 128 (one scale
+// block), where that leaves fewer warps without a block.
+template <int WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_down(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ MoeArgs a, Ring ring, Ws ws) {
     constexpr int ROW = kMoeMaxTokens + 1;  // floats of an output row's sums (odd: rows fall into different banks)
-    constexpr int WARP_SUMS = kTile * ROW, PER = kPart / (32 * kConsumers);
-    static_assert(kConsumers * WARP_SUMS <= kRed && PER * 32 * kConsumers == kPart, "sums of a tile");
+    constexpr int TILE = tile_rows(WIDE), PART = TILE * kMoeMaxTokens;
+    constexpr int WARP_SUMS = kOwn * ROW, PER = PART / (32 * kConsumers);
+    constexpr int BOXES = 16 / WIDE;  // of a slot; two slots per step
+    static_assert(WIDE == 4 || WIDE == 8, "a tile lies in one scale block and a slot holds 32 KB");
+    static_assert(kConsumers * WARP_SUMS <= kRed && PER * 32 * kConsumers == PART, "sums of a tile");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int slot_bytes = 2 * ring.blocks * 16 * SB;
+    const int box_bytes = ring.box_bytes(), slot_bytes = BOXES * box_bytes;
     float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
     float *sums = red + kRed;
     float *coef = sums;  // [pair]: routing weight x the undone power of two
@@ -630,9 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     route(a, R, reinterpret_cast<uint32_t *>(red));  // the logits were there before the previous kernel started
 
-    // this CTA's share of the (64-row tile, expert, K step) sequence; no share
+    // this CTA's share of the (tile, expert, K step) sequence; no share
     // is empty, which the count of a shared tile's shares relies on
-    const int steps = R->active * ring.steps, all = steps * (H / kTile);  // of one tile, of all
+    const int steps = R->active * ring.steps, all = steps * (H / TILE);  // of one tile, of all
     const int shares = max(min((int)gridDim.x, all), 1);
     const Share mine = (int)blockIdx.x < shares ? share_of(all, blockIdx.x, shares) : Share{all, all};
     const int u_begin = mine.begin, u_end = mine.end;
@@ -646,10 +661,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = u_begin - tile * steps;
             int ai = st / ring.steps, q = st - ai * ring.steps;
             for (int u = u_begin; u < u_end && ok; u++) {
-                const int row = (int)R->expert[ai] * H + kTile * tile;
-                for (int h = 0; h < kTile / 32 && ok; h++)
-                    ok = give.give(S, base, slot_bytes, ring.slots, &tmW, row + 32 * h, row + 32 * h + 16,
-                                   q * ring.blocks * 2);
+                const int row = (int)R->expert[ai] * H + TILE * tile;
+                for (int h = 0; h < 2 && ok; h++)
+                    ok = give.give<BOXES>(S, base, box_bytes, ring.slots, &tmW, row + 16 * BOXES * h, 16, q * ring.blocks * 2);
                 if (++q == ring.steps) {
                     q = 0;
                     if (++ai == R->active) {
@@ -708,6 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7, ib = I >> 7;
+    // A warp takes scale block wb of a step, and rows 32 wr .. + 31 of each slot.
+    const int wb = warp % WIDE, wr = warp / WIDE;
+    const int offset = 2 * wr * box_bytes + wb * 2 * 16 * CH;
     // A step's input of this lane: its token's act, 2 x 16 FP16 values, the
     // exponents of the block's eight groups, and the block's weight scale.
     struct Input {
@@ -730,15 +747,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto load = [&](const Pos &p, Input &o) {
         // (past the end of K some other valid values, not used; no branch)
-        const int kb = min(p.q * ring.blocks + warp, ib - 1);
+        const int kb = min(p.q * ring.blocks + wb, ib - 1);
         const uint32_t col = R->column[p.ai][g];
         const int pair = col == kNoColumn ? 0 : (int)(col & 0xFFFFu);
         const __half *src = ws.act + (int64_t)pair * I + kb * SB + 16 * t;
 #pragma unroll
         for (int c = 0; c < 2; c++) ld_32b_if(col != kNoColumn, src + CH * c, o.v[c]);
         o.ex = __ldcg(reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)pair * (I >> 4)) + kb);
-        // the tile's rows lie in one scale block
-        o.sc = __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * kTile / 128) * ib + kb);
+        // (the tile's rows lie in one scale block)
+        o.sc = __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * TILE / 128) * ib + kb);
     };
     // act brought to its row's power of two: a factor of 2^-d, exact down to
     // FP16's subnormals
@@ -753,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
 
-    // This warp's sums of the tile, [row][token]; an expert's products gather
+    // This warp's sums of its rows of the tile, [row][token]; an expert's products gather
     // in registers over its K steps and are added here, weighted, per token.
     float *own = red + warp * WARP_SUMS;
     auto clear = [&] {
@@ -767,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cur.ai = st / ring.steps;
     cur.q = st - cur.ai * ring.steps;
     int first = st;  // the tile's first step here
-    float acc[kTile / 16][4] = {};
+    float acc[kOwn / 16][4] = {};
     clear();
     Input in;  // one step ahead
     ahead = cur;
@@ -780,14 +797,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum[PER];
 #pragma unroll
         for (int h = 0; h < PER; h++) {
-            const int v = threadIdx.x + h * 32 * kConsumers;
+            const int v = threadIdx.x + h * 32 * kConsumers, r = v >> 4;
+            // slot r / SLOT's row 32 wr + i is row 32 (r / SLOT) + i of the warps with that wr
+            constexpr int SLOT = 16 * BOXES;
+            const float *from =
+                red + r % SLOT / 32 * WIDE * WARP_SUMS + (r / SLOT * 32 + (r & 31)) * ROW + (v & 15);
             sum[h] = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kConsumers; w++) sum[h] += red[w * WARP_SUMS + (v >> 4) * ROW + (v & 15)];
+            for (int w = 0; w < WIDE; w++) sum[h] += from[w * WARP_SUMS];
         }
         if (shared) {
             const int b0 = share_at(all, tile * steps, shares), b1 = share_at(all, (tile + 1) * steps - 1, shares);
-            float *part = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * kPart;
+            float *part = ws.part + ((int64_t)blockIdx.x * 2 + (first == 0)) * PART;
 #pragma unroll
             for (int h = 0; h < PER; h++) __stcg(part + threadIdx.x + h * 32 * kConsumers, sum[h]);
             __threadfence();
@@ -798,12 +819,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __threadfence();
 #pragma unroll
                 for (int h = 0; h < PER; h++) sum[h] = 0.0f;
-                for (int b = b0; b <= b1; b++) {
-                    // a share's slot: 1 where it has the tile's first step
-                    const int head = share_of(all, b, shares).begin <= tile * steps;
-                    const float *p = ws.part + ((int64_t)b * 2 + head) * kPart + threadIdx.x;
+                // (of its two slots the share with the tile's first step took
+                // 1, the others 0; four shares' loads are in flight together)
+                constexpr int JB = 4;
+                for (int b = b0; b <= b1; b += JB) {
+                    float v[JB][PER];
 #pragma unroll
-                    for (int h = 0; h < PER; h++) sum[h] += __ldcg(p + h * 32 * kConsumers);
+                    for (int j = 0; j < JB; j++) {
+                        const float *p = ws.part + ((int64_t)min(b + j, b1) * 2 + (b + j == b0)) * PART + threadIdx.x;
+#pragma unroll
+                        for (int h = 0; h < PER; h++) v[j][h] = __ldcg(p + h * 32 * kConsumers);
+                    }
+#pragma unroll
+                    for (int j = 0; j < JB; j++)
+#pragma unroll
+                        for (int h = 0; h < PER; h++)
+                            if (b + j <= b1) sum[h] += v[j][h];
                 }
             }
         }
@@ -811,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < PER; h++) {
                 const int v = threadIdx.x + h * 32 * kConsumers, m = v & 15;
-                if (m < T) a.out[(int64_t)m * H + kTile * tile + (v >> 4)] = __bfloat16_as_ushort(__float2bfloat16_rn(sum[h]));
+                if (m < T) a.out[(int64_t)m * H + TILE * tile + (v >> 4)] = __bfloat16_as_ushort(__float2bfloat16_rn(sum[h]));
             }
         }
         consumers_sync();  // everybody's sums, and the flag, have been read
@@ -826,10 +857,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sc[2] = {in.sc, in.sc};
         if (u + 1 < u_end) load(ahead, in);
         advance(ahead);
-        const bool active = warp < ring.blocks && cur.q * ring.blocks + warp < ib;
+        const bool active = wb < ring.blocks && cur.q * ring.blocks + wb < ib;
 #pragma unroll
-        for (int h = 0; h < kTile / 32; h++)
-            slot_mma(take, S, ring_at, slot_bytes, ring.slots, active, warp, lane, f, sc, acc[2 * h], acc[2 * h + 1]);
+        for (int h = 0; h < 2; h++)
+            slot_mma(take, S, ring_at, slot_bytes, ring.slots, box_bytes, offset, active, lane, f, sc, acc[2 * h],
+                     acc[2 * h + 1]);
         const int tile = cur.tile, ai = cur.ai;
         advance(cur);
         if (cur.ai == ai && cur.tile == tile && u + 1 < u_end) return;
@@ -841,12 +873,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float cf = coef[to & 0xFFFFu];
                 float *o = own + g * ROW + (to >> 16);
 #pragma unroll
-                for (int r = 0; r < kTile / 8; r++) o[8 * r * ROW] = __fmaf_rn(acc[r >> 1][2 * (r & 1) + c], cf, o[8 * r * ROW]);
+                for (int r = 0; r < kOwn / 8; r++) o[8 * r * ROW] = __fmaf_rn(acc[r >> 1][2 * (r & 1) + c], cf, o[8 * r * ROW]);
             }
         }
         __syncwarp();
 #pragma unroll
-        for (int r = 0; r < kTile / 16; r++) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
+        for (int r = 0; r < kOwn / 16; r++) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
         if (cur.tile == tile && u + 1 < u_end) return;
         finish_tile(tile, first != 0 || cur.tile == tile);
         first = 0;
@@ -859,13 +891,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr size_t kSmemMax = 232448;
 constexpr size_t kFixed = 1024 + (kRed + kSums) * 4 + sizeof(Route) + sizeof(Bars);  // all but the ring
 
-// Boxes of equal size, at most 1 KB of K, and as many slots as fit.
-Ring ring_for(int k) {
+// Boxes of equal size, at most `wide` scale blocks of K, and as many slots (of
+// `boxes` boxes) as fit.
+Ring ring_for(int k, int wide, int boxes) {
     Ring r;
     const int blocks = k / SB;
-    r.steps = (blocks + kConsumers - 1) / kConsumers;
+    r.steps = (blocks + wide - 1) / wide;
     r.blocks = (blocks + r.steps - 1) / r.steps;
-    const int room = (int)((kSmemMax - kFixed) / ((size_t)r.blocks * 2 * 16 * SB));
+    const int room = (int)((kSmemMax - kFixed) / ((size_t)boxes * r.box_bytes()));
     r.slots = room < kMaxSlots ? room : kMaxSlots;
     return r;
 }
@@ -875,8 +908,8 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
     const size_t pairs = (size_t)tokens * topk;
     const size_t act = align256(pairs * inter * sizeof(__half)), ex = align256(pairs * (inter / 16)),
-                 count = align256((size_t)hidden / kTile * sizeof(int)),
-                 part = (size_t)sm_count() * 2 * kPart * sizeof(float);
+                 count = align256((size_t)hidden / kMinTile * sizeof(int)),
+                 part = (size_t)sm_count() * 2 * kMaxTile * kMoeMaxTokens * sizeof(float);
     if (ws) {
         uint8_t *b = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 255) & ~uintptr_t(255));
         ws->act = reinterpret_cast<__half *>(b);
@@ -888,8 +921,9 @@ size_t ws_layout(void *p, int tokens, int hidden, int inter, int topk, Ws *ws) {
 }
 
 template <class F>
-cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const MoeArgs &a, const Ws &ws, cudaStream_t s) {
-    const Ring ring = ring_for(k);
+cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, int wide, int boxes, const MoeArgs &a,
+                       const Ws &ws, cudaStream_t s) {
+    const Ring ring = ring_for(k, wide, boxes);
     alignas(64) CUtensorMap tm;
     const uint64_t d[3] = {CH, (uint64_t)rows, (uint64_t)k / CH}, st[2] = {(uint64_t)k, CH};
     const uint32_t box[3] = {CH, 16, (uint32_t)(2 * ring.blocks)};
@@ -897,7 +931,7 @@ cudaError_t launch_one(F kernel, const uint8_t *w, int64_t rows, int k, const Mo
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sm_count());
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kFixed + (size_t)ring.slots * ring.blocks * 2 * 16 * SB;
+    cfg.dynamicSmemBytes = kFixed + (size_t)ring.slots * boxes * ring.box_bytes();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -928,14 +962,25 @@ cudaError_t launch_fp8_moe_blockscaled(const MoeArgs &a, cudaStream_t s) {
         const cudaError_t err =
             cudaFuncSetAttribute(k_moe_gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
         if (err != cudaSuccess) return err;
-        return cudaFuncSetAttribute(k_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+        const cudaError_t err8 =
+            cudaFuncSetAttribute(k_moe_down<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+        if (err8 != cudaSuccess) return err8;
+        return cudaFuncSetAttribute(k_moe_down<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
     });
     if (e != cudaSuccess) return e;
     Ws ws;
     ws_layout(a.workspace, a.tokens, a.hidden, a.inter, a.topk, &ws);
-    e = launch_one(k_moe_gate_up, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, a, ws, s);
+    e = launch_one(k_moe_gate_up, a.w_gu, (int64_t)a.experts * 2 * a.inter, a.hidden, kConsumers, 2, a, ws, s);
     if (e != cudaSuccess) return e;
-    return launch_one(k_moe_down, a.w_d, (int64_t)a.experts * a.hidden, a.inter, a, ws, s);
+    // Four blocks of K side by side where eight leave more warps idle (inter
+    // 1408, eleven blocks: 11 of 12 against 11 of 16; 16 tokens of 5120 x 1408
+    // x 64 experts 5.2 TB/s against 5.0), else eight, with smaller tiles to
+    // share and join (1 token, 2048 x 768 x 64: 22.3 us against 23.4).
+    const int blocks = a.inter / SB;
+    const bool four = (blocks + 3) / 4 * 4 < (blocks + 7) / 8 * 8;
+    const int64_t rows = (int64_t)a.experts * a.hidden;
+    return four ? launch_one(k_moe_down<4>, a.w_d, rows, a.inter, 4, 4, a, ws, s)
+                : launch_one(k_moe_down<8>, a.w_d, rows, a.inter, 8, 2, a, ws, s);
 }
 
 }  // namespace bsq

@@ -5,7 +5,9 @@
 Inputs are random codes in device memory (the kernel's cost does not depend
 on their values beyond power); nothing is checked.  Kinds: w4a4 (M <= 128
 runs the few-row kernel), fp8gemm, int8gemm, int8gemm_ws (with the
-tail-splitting workspace), gemv, gemv_bs (block-scaled),
+tail-splitting workspace), gemv, gemv_bs (block-scaled), fp8gemm_bs
+(block-scaled GEMM), moe (m tokens, n = 2 * inter, k = hidden, 64 experts, 8
+per token), norm_fp8, quant_fp8, silu_fp8 (n = 2k columns in),
 quant_nvfp4, quant_rowfp8, quant_int8, requant_w, requant_block.
 """
 from __future__ import annotations
@@ -66,6 +68,30 @@ def main():
     elif a.kind == "gemv":
         x, w, s = bf16((m, k)), u8((n, k), 0, 0x7F), torch.rand(n, device=dev)
         fn = lambda: bsq.fp8_gemv_rowscale(x, w, s, out, m, n, k)
+    elif a.kind == "fp8gemm_bs":
+        x, w, out = u8((m, k), 0, 0x7F), u8((n, k), 0, 0x7F), bf16((m, n))
+        sa, sw = torch.rand(m, k // 128, device=dev), torch.rand((n + 127) // 128, k // 128, device=dev)
+        fn = lambda: bsq.fp8_gemm_blockscaled(x, sa, w, sw, out, m, n, k)
+    elif a.kind == "moe":
+        experts, topk, inter = 64, 8, n // 2
+        x, logits, out = bf16((m, k)), torch.randn(m, experts, device=dev, generator=g), bf16((m, k))
+        w13, w2 = u8((experts, n, k), 0, 0x7F), u8((experts, k, inter), 0, 0x7F)
+        s13 = torch.rand(experts, n // 128, k // 128, device=dev) * 1e-4
+        s2 = torch.rand(experts, k // 128, inter // 128, device=dev)
+        nb = bsq.fp8_moe_workspace_bytes(m, k, inter, topk)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        fn = lambda: bsq.fp8_moe_blockscaled(x, logits, w13, s13, w2, s2, out, None, None, ws, nb, m, k, inter, experts,
+                                             topk, 1)
+    elif a.kind == "norm_fp8":
+        x, r, gain = bf16((m, k)), bf16((m, k)), bf16((k,))
+        q, s = u8((m, k)), torch.empty((m, k // 128), device=dev)
+        fn = lambda: bsq.rmsnorm_residual_quant_fp8(x, r, gain, 1e-6, r, q, s, 128, m, k)
+    elif a.kind == "quant_fp8":
+        x, q, s = bf16((m, k)), u8((m, k)), torch.empty((m, k // 128), device=dev)
+        fn = lambda: bsq.quant_act_fp8_per128(x, q, s, m, k)
+    elif a.kind == "silu_fp8":
+        x, q, s = bf16((m, 2 * k)), u8((m, k)), torch.empty((m, k // 128), device=dev)
+        fn = lambda: bsq.silu_mul_quant_fp8_per128(x, q, s, m, k)
     elif a.kind == "quant_nvfp4":
         x = bf16((m, k))
         p_, s_ = u8((m, k // 2)), u8((m, k // 16))
