@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) k_silu_mul_quant_fp8_per128(const ui
 // ---------------------------------------------------------------------------
 // RMS norm.  A row is held in registers as BF16 between the sum of squares and
 // the codes, KEEP units per thread: one warp per row (eight rows per CTA, no
-// barrier) where it fits, else one CTA per row.
+// barrier) up to K = 1024, else one CTA per row.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -331,6 +331,14 @@ cudaError_t launch_rmsnorm_residual_quant_fp8(const uint16_t *x, const uint16_t 
     };
     if (units <= 32) return warp_rows(k_rmsnorm_residual_quant_fp8<1, true>);
     if (units <= 64) return warp_rows(k_rmsnorm_residual_quant_fp8<2, true>);
+    // One unit per thread for short rows (8192 x 1040: 16.6 us, 19.0 with two),
+    // for no more rows than SMs (1 x 5120: 2.6 us, 3.4 with two), and where all
+    // rows of a medium length are resident at once (300 x 5120: 4.6 us, 5.4
+    // with two); else two, which keep more loads in flight per warp (8192 x
+    // 5120: 48.6 us, 51.7 with one; 1000 x 16384: 24.0 us, 30.0 with one).
+    const int64_t sms = sm_count();
+    if (units <= 160 || (units <= 384 && (int64_t)m * units <= 1024 * sms) || (units <= 1024 && m <= sms))
+        return cta_rows(k_rmsnorm_residual_quant_fp8<1, false>, 1);
     if (units <= 1024 * 2) return cta_rows(k_rmsnorm_residual_quant_fp8<2, false>, 2);
     return cta_rows(k_rmsnorm_residual_quant_fp8<4, false>, 4);
 }
