@@ -51,18 +51,57 @@ __device__ __forceinline__ void unpack_unit(const Unit &v, float (&y)[16]) {
     }
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
+    return p;
+}
+// E4M3 codes of four values, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b) {
+    return (uint32_t)f32x2_to_e4m3x2(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)(a >> 32))) |
+           (uint32_t)f32x2_to_e4m3x2(__uint_as_float((uint32_t)b), __uint_as_float((uint32_t)(b >> 32))) << 16;
+}
+
 // Sixteen E4M3 codes of y / s; s == 0 (an all-zero group) gives zeros.
+// With r = rcp.approx(s), within 2^-23, the products y r (1 -+ 2^-20) lie on
+// either side of RN(y / s) (their own roundings are 2^-24 each): where the
+// codes of both agree they are the answer, for all sixteen in one comparison.
+// Otherwise the pairs that differ are settled one by one.  (A branch per pair,
+// at 2^-16, instead: SiLU 2048 x 17408 37.8 us, 34.7 so; norm 8192 x 5120 48.1
+// and 46.5.)
 __device__ __forceinline__ uint4 codes_16(const float (&y)[16], float s) {
     if (s == 0.0f) return make_uint4(0u, 0u, 0u, 0u);
     const Bracket br = bracket_of(s);
-    float lo[8], hi[8];
+    uint32_t w[4];
+    if (br.ok) {
+        const float l = __fmul_rn(br.r, 1.0f - 0x1p-20f), h = __fmul_rn(br.r, 1.0f + 0x1p-20f);
+        const uint64_t ll = f32x2_pack(l, l), hh = f32x2_pack(h, h);
+        uint32_t d[4];  // bits in which the two codes differ
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        lo[i] = y[i];
-        hi[i] = y[8 + i];
+        for (int j = 0; j < 4; j++) {
+            const uint64_t a = f32x2_pack(y[4 * j], y[4 * j + 1]), b = f32x2_pack(y[4 * j + 2], y[4 * j + 3]);
+            w[j] = e4m3x4(mul2(a, ll), mul2(b, ll));
+            d[j] = w[j] ^ e4m3x4(mul2(a, hh), mul2(b, hh));
+        }
+        if ((d[0] | d[1] | d[2] | d[3]) != 0u) {
+#pragma unroll
+            for (int p = 0; p < 8; p++) {
+                const uint32_t dp = (d[p >> 1] >> (16 * (p & 1))) & 0xFFFFu;
+                if (dp != 0u) {
+                    float p0 = __fmul_rn(y[2 * p], l), p1 = __fmul_rn(y[2 * p + 1], l);
+                    pair_boundaries<5, 8>(y[2 * p], y[2 * p + 1], s, p0, p1, 0u, dp);
+                    const uint32_t c = f32x2_to_e4m3x2(p0, p1);
+                    w[p >> 1] = p & 1 ? (w[p >> 1] & 0xFFFFu) | c << 16 : (w[p >> 1] & 0xFFFF0000u) | c;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            w[j] = (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(y[4 * j], s), __fdiv_rn(y[4 * j + 1], s)) |
+                   (uint32_t)f32x2_to_e4m3x2(__fdiv_rn(y[4 * j + 2], s), __fdiv_rn(y[4 * j + 3], s)) << 16;
     }
-    const uint2 a = e4m3_codes_8(lo, s, br), b = e4m3_codes_8(hi, s, br);
-    return make_uint4(a.x, a.y, b.x, b.y);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ float amax_16(const float (&y)[16]) {
