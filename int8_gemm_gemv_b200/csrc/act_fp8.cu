@@ -332,10 +332,10 @@ cudaError_t launch_pss(void (*kernel)(P...), int64_t grid, int threads, cudaStre
     return e;
 }
 
-// Units per lane: two where that still gives every SM its fill of threads
-// (quantiser 4096 x 17408: 47.8 us, 49.8 with one; 63.7 with four), one below
-// (16 x 5120: 2.2 us, 3.1 with two).
-bool two_units(int64_t units) { return units >= (int64_t)sm_count() * 2048; }
+// Units per lane: two where that still gives the SMs three times the threads
+// they hold or more (quantiser 4096 x 17408: 39.6 us, 44.0 with one, 55.0 with
+// four), one below (512 x 17408: 6.8 us, 7.4 with two).
+bool two_units(int64_t units) { return units >= (int64_t)sm_count() * 2048 * 3; }
 int64_t grid_for_units(int64_t units, int unroll) { return (units + (int64_t)kThreads * unroll - 1) / (kThreads * unroll); }
 
 }  // namespace

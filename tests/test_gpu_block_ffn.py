@@ -97,6 +97,27 @@ def test_quant_act_codes_are_the_oracles(m, k):
     assert (q[m] == 0xFF).all() and s[m].isnan().all()  # nothing behind the last row
 
 
+def test_quant_act_on_code_boundaries():
+    """Values at, and one BF16 step either side of, every boundary between two
+    codes, for every BF16 mantissa of amax: ties and near-ties."""
+    codes_up = torch.arange(0x7F, dtype=torch.uint8).view(F8).double()  # 0 .. 448
+    mid = (codes_up[1:] + codes_up[:-1]) / 2  # 126 of them
+    top = (1 + torch.arange(128) / 128).double()
+    amax = torch.cat([top * 2.0**e for e in (-125, -60, -52, 0, 7, 66, 127)])
+    x = (amax[:, None] * mid / 448).bfloat16()
+    x = torch.cat([x, torch.zeros(len(amax), 1), amax[:, None]], 1).bfloat16()
+    x = torch.cat([torch.where(x.view(torch.int16) + d >= 0, x.view(torch.int16) + d, 0).view(torch.bfloat16)
+                   for d in (-1, 0, 1)])
+    x[:, 127] = amax.bfloat16().repeat(3)
+    x[:, :126:2] *= -1
+    assert torch.equal(x.abs().amax(1).double(), amax.repeat(3))
+    q, s = poisoned(x.shape, torch.uint8), poisoned((len(x),), torch.float32)
+    bsq.quant_act_fp8_per128(x.to(DEV), q, s, len(x), 128)
+    oq, os_ = oracle.quant_rowwise_fp8(x.view(torch.int16).numpy().view(np.uint16))
+    assert np.array_equal(s.cpu().numpy(), os_)
+    assert np.array_equal(q.cpu().numpy(), oq)
+
+
 # ---------------------------------------------------------- silu * mul ---
 
 @pytest.mark.parametrize("m,k", [(1, 128), (5, 17408), (64, 1408), (333, 256), (3, 512)])
