@@ -6,11 +6,15 @@
 //
 // The reached experts' weights, read once, are the whole cost, so both kernels
 // are streaming reads built like the FP8 GEMV: one CTA per SM, a TMA producer
-// warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, two
-// boxes to a slot, and eight consumer warps that split a box's K into its
+// warp that fills a ring with boxes of 16 weight rows x up to 1 KB of K, up to
+// 32 KB to a slot, and eight consumer warps that split a box's K into its
 // 128-wide scale blocks (E4M3 -> FP16 exactly, FP16 MMAs with FP32 sums, each
 // block's sum times its scale).  The MMA's eight columns are tokens that chose
 // the expert (more than eight: it is listed, and read, twice).
+// Measured: 16 tokens, 57 of 64 experts of 5120 x 1408 reached: 237 us, 5.2
+// TB/s, of which the routing takes 6, the activations' maxima 7 and the
+// exponents of act 5; 1 token, 2048 x 768, 64 experts, 8 choices: 22.5 us, two
+// kernels' latency around some 6 us of streaming.
 //
 //   k_moe_gate_up  every CTA routes all tokens by itself (some hundred
 //                  instructions per token), then takes an equal share of the
@@ -18,7 +22,7 @@
 //                  and one of up rows give silu(g) * u on the spot.  act is
 //                  kept as FP16 times a power of two per 16 values, 11
 //                  significant bits.
-//   k_moe_down     an output tile of 64 rows runs over all reached experts'
+//   k_moe_down     an output tile of 64 or 128 rows runs over all reached experts'
 //                  K, so a token's experts add up in registers.  The (tile,
 //                  expert, K) steps are cut into equal shares, one per CTA,
 //                  also inside a tile: the 80 tiles of 5120 outputs alone
