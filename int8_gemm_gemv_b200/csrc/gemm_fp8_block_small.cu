@@ -40,7 +40,10 @@ static __device__ unsigned int g_timeouts;
 template <int NT> struct Cfg {
     static constexpr int A_BYTES = NT * BK, STAGE_BYTES = W_BYTES + A_BYTES;
     static constexpr int NBUF = 4;
-    static constexpr int TMEM_COLS = NBUF * NT;  // 64 or 128
+    // 64 or 128 of 512: at most three CTAs of 384 threads fit an SM's registers,
+    // so none of a cluster ever waits for columns that another cluster's CTA
+    // holds while that one waits for its own peers
+    static constexpr int TMEM_COLS = NBUF * NT;
     static constexpr int CW = NT / 2;            // columns of one fold warp
 };
 

@@ -608,3 +608,38 @@ def test_two_calls_at_once():
         a(s1), b(s2), f(s1), g(s2)
     torch.cuda.synchronize()
     a.check(), b.check(), f.check(), g.check()
+
+
+def test_many_streams_same_bits():
+    """Every operator on a stream of its own, several launches in flight on
+    each: the same bits as alone."""
+    def gemm(m, n, k, seed):
+        a, w = codes((m, k), seed), codes((n, k), seed + 1)
+        sa, sw = scales((m, k // 128), 1), scales(((n + 127) // 128, k // 128), 2)
+        out = poisoned((m, n), torch.bfloat16)
+        return (lambda st: bsq.fp8_gemm_blockscaled(a, sa, w, sw, out, m, n, k, st)), out
+
+    jobs = [gemm(700, 5120, 2048, 1), gemm(16, 5120, 5120, 3), gemm(40, 2112, 5120, 5), gemm(3, 1024, 5120, 7),
+            gemm(300, 4097, 1024, 9)]
+    for seed in (1, 2):
+        layer = Moe(5 * seed, 1024, 768, 12, 3, 1, seed=seed)
+        jobs.append((layer, layer.out))
+    x = activations(500, 5120, 3)
+    q, s = poisoned((500, 5120), torch.uint8), poisoned((500, 40), torch.float32)
+    jobs.append((lambda st: bsq.rmsnorm_residual_quant_fp8(x, None, x[0], 1e-6, None, q, s, 128, 500, 5120, st), q))
+    want = []
+    for call, out in jobs:
+        call(None)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(10):
+        for _, out in jobs:
+            out.view(torch.uint8).fill_(0xFF)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for st, (call, _) in zip(streams, jobs):
+                call(st)
+        torch.cuda.synchronize()
+        for (_, out), w in zip(jobs, want):
+            assert torch.equal(out.view(torch.uint8), w.view(torch.uint8))
