@@ -473,8 +473,11 @@ BSQ_API bsq_status fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, 
  * output of zeros.  An expert whose weight is 0 is not read for that token.
  *   act = (g / (1 + exp(-g))) * u, g and u the gate and up products;
  *   out[t] = sum_j weight[t,j] * (w_down[id_j] act_j)
- * FP32 sums, one BF16 rounding; act is kept with 11 significant bits or
- * more.  An output does not change from run to run.
+ * FP32 sums, one BF16 rounding.  Activations enter as in fp8_gemv_rowscale:
+ * exact within 2^31 of their token's largest magnitude, smaller ones rounded
+ * by less than 2^-39 of it.  An act value is rounded by at most 2^-11 of
+ * itself plus 2^-38 of the largest of its expert's 128 (a scale block of
+ * w_down's K).  An output does not change from run to run.
  * Errors: tokens outside 0..16, experts <= 0, topk outside 1..experts,
  * hidden or inter not a positive multiple of 16, renormalise not 0 or 1,
  * ws_bytes too small -> INVALID_ARG; hidden or inter not a multiple of 128,

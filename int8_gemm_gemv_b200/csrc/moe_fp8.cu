@@ -11,19 +11,24 @@
 // 128-wide scale blocks (E4M3 -> FP16 exactly, FP16 MMAs with FP32 sums, each
 // block's sum times its scale).  The MMA's eight columns are tokens that chose
 // the expert (more than eight: it is listed, and read, twice).
-// Measured: 16 tokens, 57 of 64 experts of 5120 x 1408 reached: 237 us, 5.2
-// TB/s, of which the routing takes 6, the activations' maxima 7 and the
-// exponents of act 5; 1 token, 2048 x 768, 64 experts, 8 choices: 22.5 us, two
-// kernels' latency around some 6 us of streaming.
+// Measured (back to back in a graph): 16 tokens, 57 of 64 experts of 5120 x
+// 1408 reached: 230 us, 5.3 TB/s, of which the routing takes 6 and the
+// activations' maxima 7; 1 token, 2048 x 768, 64 experts, 8 choices: 20.7 us,
+// two kernels' latency around some 6 us of streaming.
 //
 //   k_moe_gate_up  every CTA routes all tokens by itself (some hundred
 //                  instructions per token), then takes an equal share of the
 //                  (expert, 16 intermediate rows) pairs: a box of gate rows
 //                  and one of up rows give silu(g) * u on the spot.  act is
 //                  kept as FP16 times a power of two per 16 values, 11
-//                  significant bits.
+//                  significant bits: the down product's MMAs are FP16, and a
+//                  second FP16 for the rest would double them for less than a
+//                  tenth of the output's own BF16 rounding.
 //   k_moe_down     an output tile of 64 or 128 rows runs over all reached experts'
-//                  K, so a token's experts add up in registers.  The (tile,
+//                  K, so a token's experts add up in registers.  act enters
+//                  the MMAs at one power of two per token and scale block,
+//                  undone in the FP32 fold of that block, so a block's bits do
+//                  not depend on how large the others are.  The (tile,
 //                  expert, K) steps are cut into equal shares, one per CTA,
 //                  also inside a tile: the 80 tiles of 5120 outputs alone
 //                  would occupy 80 of 148 SMs.  CTAs that share a tile leave
@@ -61,8 +66,7 @@ constexpr int kSums = 512;     // floats of a group's sums: tiles x 16 rows x 8 
 constexpr int kOwn = 64;
 constexpr int tile_rows(int wide) { return kOwn * kConsumers / wide; }
 constexpr int kMinTile = tile_rows(8), kMaxTile = tile_rows(4);
-static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums && 2 * kMaxActive <= kSums && kMaxActive + 1 <= 4 * (kSums - kMaxActive),
-              "shared buffers");
+static_assert(kRed >= kMoeMaxTokens * kMoeMaxExperts && kRed >= kConsumers * kSums, "shared buffers");
 
 static __device__ unsigned int g_timeouts;
 
@@ -311,9 +315,13 @@ __device__ __forceinline__ void chunk_mma_8(float (&d)[4], const uint4 &wa, cons
 // Two boxes of the next slot: acc[box] += scale[box] * (this warp's scale
 // block, two chunks, of the box) x the activation fragments x[chunk], as four
 // independent chains of MMAs.  `offset` is that block's place in the slot.
+// With COLS the sums of the lane's two columns (tokens) are also multiplied by
+// col, powers of two.
+template <bool COLS>
 __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, int slot_bytes, int slots, int box_bytes,
                                          int offset, bool active, int lane, const uint32_t (&x)[2][8],
-                                         const float (&scale)[2], float (&acc0)[4], float (&acc1)[4]) {
+                                         const float (&scale)[2], const float (&col)[2], float (&acc0)[4],
+                                         float (&acc1)[4]) {
     const uint32_t at = take.take(S, ring, slot_bytes) + offset;
     const int g = lane >> 2, t = lane & 3;
     uint4 w[2][2][2];  // [box][chunk][row g, g + 8]
@@ -336,8 +344,9 @@ __device__ __forceinline__ void slot_mma(Taker &take, Bars *S, uint32_t ring, in
         for (int v = 0; v < 2; v++) chunk_mma_8(d[v][c], w[v][c][0], w[v][c][1], x[c]);
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        acc0[k] = __fmaf_rn(d[0][0][k] + d[0][1][k], scale[0], acc0[k]);
-        acc1[k] = __fmaf_rn(d[1][0][k] + d[1][1][k], scale[1], acc1[k]);
+        const float d0 = d[0][0][k] + d[0][1][k], d1 = d[1][0][k] + d[1][1][k];
+        acc0[k] = COLS ? __fmaf_rn(d0 * scale[0], col[k & 1], acc0[k]) : __fmaf_rn(d0, scale[0], acc0[k]);
+        acc1[k] = COLS ? __fmaf_rn(d1 * scale[1], col[k & 1], acc1[k]) : __fmaf_rn(d1, scale[1], acc1[k]);
     }
 }
 
@@ -429,8 +438,8 @@ struct Ws {
     float *part;       // [CTAs][2][tile rows x tokens] FP32 sums of shared tiles
 };
 
-// The power of two for 16 (or a row of) act values whose largest has this
-// FP32 exponent field: brings it to [2^14, 2^15).
+// The power of two for 16 (or a scale block of) act values whose largest has
+// this FP32 exponent field: brings it to [2^14, 2^15).
 __device__ __forceinline__ int exp_shift(int e) { return min(14 - (e - 127), 127); }
 
 // ---------------------------------------------------------------- gate, up --
@@ -579,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int p = 0; p < PG; p++) {
                 if (p >= n) break;
-                slot_mma(take, S, ring_at, slot_bytes, ring.slots, box_bytes, warp * 2 * 16 * CH, active, lane, f, sc[p],
-                         acc[2 * p], acc[2 * p + 1]);
+                slot_mma<false>(take, S, ring_at, slot_bytes, ring.slots, box_bytes, warp * 2 * 16 * CH, active, lane, f,
+                                sc[p], {1.0f, 1.0f}, acc[2 * p], acc[2 * p + 1]);
             }
         }
         reduce_warps<TG>(acc, red, sums, warp, lane, 2 * n * 128);
@@ -637,11 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int box_bytes = ring.box_bytes(), slot_bytes = BOXES * box_bytes;
     float *red = reinterpret_cast<float *>(base + (size_t)ring.slots * slot_bytes);
-    float *sums = red + kRed;
-    float *coef = sums;  // [pair]: routing weight x the undone power of two
-    Route *R = reinterpret_cast<Route *>(sums + kSums);
+    Route *R = reinterpret_cast<Route *>(red + kRed);
     Bars *S = reinterpret_cast<Bars *>(R + 1);
-    int8_t *shift = reinterpret_cast<int8_t *>(sums + kMaxActive);  // [pair]: its row's power of two
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.hidden, I = a.inter, T = a.tokens;
@@ -691,38 +697,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.out[i] = 0;
         return;
     }
-    // every (token, choice)'s power of two, from its groups' exponents
-    const int pairs = T * a.topk;
-    constexpr int PB = 8;  // pairs of a warp whose loads are in flight together
-    for (int p0 = warp; p0 < pairs; p0 += PB * kConsumers) {
-        uint32_t mx[PB];
-#pragma unroll
-        for (int i = 0; i < PB; i++) mx[i] = 0;
-        for (int k = lane; k < (I >> 7); k += 32) {
-            uint2 v[PB];
-#pragma unroll
-            for (int i = 0; i < PB; i++) {
-                const int p = min(p0 + i * kConsumers, pairs - 1);
-                v[i] = __ldcg(reinterpret_cast<const uint2 *>(ws.act_exp + (int64_t)p * (I >> 4)) + k);
-            }
-#pragma unroll
-            for (int i = 0; i < PB; i++) mx[i] = __vmaxu4(mx[i], __vmaxu4(v[i].x, v[i].y));
-        }
-#pragma unroll
-        for (int i = 0; i < PB; i++) {
-            const int p = p0 + i * kConsumers;
-            mx[i] = __vmaxu4(mx[i], mx[i] >> 16);
-            mx[i] = __reduce_max_sync(0xFFFFFFFFu, max(mx[i] & 0xFFu, (mx[i] >> 8) & 0xFFu));
-            // (a pair of weight 0 has no act, and no column refers to it)
-            if (lane == 0 && p < pairs) {
-                const int s = exp_shift((int)mx[i]);
-                shift[p] = (int8_t)s;
-                coef[p] = R->weight[p / a.topk][p % a.topk] * pow2i(-s);
-            }
-        }
-    }
-    consumers_sync();
-
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring_at = smem_u32(base);
     const int hb = H >> 7, ib = I >> 7;
@@ -761,15 +735,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (the tile's rows lie in one scale block)
         o.sc = __ldg(a.s_d + ((int64_t)R->expert[p.ai] * hb + p.tile * TILE / 128) * ib + kb);
     };
-    // act brought to its row's power of two: a factor of 2^-d, exact down to
-    // FP16's subnormals
-    auto to_row = [&](const uint32_t(&v)[8], uint32_t exps, int row_exp, uint32_t(&o)[8]) {
-        const int d = min(max(exp_shift((int)((exps >> (8 * t)) & 0xFFu)) - row_exp, 0), 40);
-        const __half f = __float2half_rn(__uint_as_float((uint32_t)(127 - d) << 23));  // 2^-d, 0 from 2^-25 on
-        const __half2 f2 = __half2half2(f);
+    // Sixteen act values brought to their scale block's power of two, which the
+    // fold undoes: the factor 2^-d, exact down to FP16's subnormals (2^-24,
+    // where the block's largest is 2^14 or more; a whole block may be as far
+    // from another as FP32 goes).  From 2^-25 on FP16 has no such factor, so it
+    // is taken as two.
+    auto to_block = [&](const uint32_t(&v)[8], uint32_t exps, int block_shift, uint32_t(&o)[8]) {
+        const int d = min(max(exp_shift((int)((exps >> (8 * t)) & 0xFFu)) - block_shift, 0), 40), d0 = min(d, 24);
+        const __half2 f0 = __float2half2_rn(pow2i(-d0)), f1 = __float2half2_rn(pow2i(d0 - d));
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&v[j]), f2);
+            const __half2 h = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&v[j]), f1), f0);
             o[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
     };
@@ -853,19 +829,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         clear();
     };
     auto step = [&](int u) {
-        const uint32_t col = R->column[cur.ai][g];
-        const int row_exp = col == kNoColumn ? 127 : shift[col & 0xFFFFu];  // (without a token: zeros)
+        // the block's largest exponent, its power of two, and how that is undone
+        // for this lane's columns 2t and 2t + 1 (without a token: zeros times
+        // some power of two)
+        uint32_t mx = __vmaxu4(in.ex.x, in.ex.y);
+        mx = __vmaxu4(mx, mx >> 16);
+        const int shift = exp_shift((int)max(mx & 0xFFu, (mx >> 8) & 0xFFu));
+        const float undo = pow2i(-shift);
+        const float cols[2] = {__shfl_sync(0xFFFFFFFFu, undo, 8 * t), __shfl_sync(0xFFFFFFFFu, undo, 8 * t + 4)};
         uint32_t f[2][8];
 #pragma unroll
-        for (int c = 0; c < 2; c++) to_row(in.v[c], c ? in.ex.y : in.ex.x, row_exp, f[c]);
+        for (int c = 0; c < 2; c++) to_block(in.v[c], c ? in.ex.y : in.ex.x, shift, f[c]);
         const float sc[2] = {in.sc, in.sc};
         if (u + 1 < u_end) load(ahead, in);
         advance(ahead);
         const bool active = wb < ring.blocks && cur.q * ring.blocks + wb < ib;
 #pragma unroll
         for (int h = 0; h < 2; h++)
-            slot_mma(take, S, ring_at, slot_bytes, ring.slots, box_bytes, offset, active, lane, f, sc, acc[2 * h],
-                     acc[2 * h + 1]);
+            slot_mma<true>(take, S, ring_at, slot_bytes, ring.slots, box_bytes, offset, active, lane, f, sc, cols,
+                           acc[2 * h], acc[2 * h + 1]);
         const int tile = cur.tile, ai = cur.ai;
         advance(cur);
         if (cur.ai == ai && cur.tile == tile && u + 1 < u_end) return;
@@ -874,8 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; c++) {
             const uint32_t to = R->column[ai][2 * t + c];
             if (to != kNoColumn) {
-                const float cf = coef[to & 0xFFFFu];
-                float *o = own + g * ROW + (to >> 16);
+                const int m = (int)(to >> 16);
+                const float cf = R->weight[m][(int)(to & 0xFFFFu) - m * a.topk];
+                float *o = own + g * ROW + m;
 #pragma unroll
                 for (int r = 0; r < kOwn / 8; r++) o[8 * r * ROW] = __fmaf_rn(acc[r >> 1][2 * (r & 1) + c], cf, o[8 * r * ROW]);
             }
