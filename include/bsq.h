@@ -398,8 +398,10 @@ BSQ_API bsq_status fp8_gemm_rowscale(const uint8_t *a, const float *a_scale,
  *   y = (h * r) * gain, r = 1 / sqrt(sum h^2 / k + eps), all in FP32 and not
  *   rounded further; s = amax|y| / 448 over each group; q =
  *   E4M3_rne_satfinite(y / s); an all-zero group gives s = 0 and q = 0.
- *   sum h^2 must stay finite in FP32; a square below its range counts as 0,
- *   and a row whose squares all do gives zeros where eps = 0.
+ *   sum h^2 must stay finite in FP32: a row where it does not, or that holds a
+ *   NaN, gets NaN in all its codes and scales (a NaN gain in its groups').  A
+ *   square below FP32's normal range loses bits or counts as 0, and a row
+ *   whose squares all do the latter gives zeros where eps = 0.
  *   x, residual, gain, residual_out, q 16-byte aligned, scale 4-byte.
  * Errors: k % 16 != 0, group not 0 or 128, group 128 with k % 128 != 0, eps
  * negative or not finite -> INVALID_ARG; k > 65536 -> UNSUPPORTED.
@@ -414,7 +416,8 @@ BSQ_API bsq_status rmsnorm_residual_quant_fp8(const uint16_t *x, const uint16_t 
  * activations of fp8_gemm_blockscaled (per token and 128 of K; the weight's
  * 128 x 128 blocks are quant_blockfp8's).
  *   Per group: s = amax / 448 (FP32); q = E4M3_rne_satfinite(x / s);
- *   amax = 0 gives s = 0 and q = 0.
+ *   amax = 0 gives s = 0 and q = 0, a NaN gives NaN in the group's codes and
+ *   scale.
  * Errors: k % 128 != 0 -> INVALID_ARG.  a, a_fp8 16-byte aligned.
  * ---------------------------------------------------------------------- */
 BSQ_API bsq_status quant_act_fp8_per128(const uint16_t *a, uint8_t *a_fp8, float *a_scale,
@@ -425,7 +428,8 @@ BSQ_API bsq_status quant_act_fp8_per128(const uint16_t *a, uint8_t *a_fp8, float
  * the down projection: gate_up BF16 [m, 2k] (the gate's k columns, then the
  * up projection's k) -> E4M3 [m, k] + FP32 [m, k/128].
  *   y = (g / (1 + exp(-g))) * u in FP32, not rounded further, then the codes
- *   and scales of quant_act_fp8_per128 on y.  |y| must stay finite.
+ *   and scales of quant_act_fp8_per128 on y.  |y| must stay finite; a NaN
+ *   gives NaN in its group's codes and scale.
  * Errors: k % 128 != 0 -> INVALID_ARG.  gate_up, a_fp8 16-byte aligned.
  * ---------------------------------------------------------------------- */
 BSQ_API bsq_status silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *a_fp8,

@@ -104,17 +104,26 @@ __device__ __forceinline__ uint4 codes_16(const float (&y)[16], float s) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The larger value, NaN where either is: a group with a NaN gets a NaN scale
+// and NaN codes, as in the quantiser, whose maximum of the BF16 bits ranks NaN
+// highest.  (fmaxf drops NaN, and a group of nothing else would become zeros.)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 __device__ __forceinline__ float amax_16(const float (&y)[16]) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; i++) m = fmaxf(m, fabsf(y[i]));
+    for (int i = 0; i < 16; i++) m = max_nan(m, fabsf(y[i]));
     return m;
 }
 
 // Max over the eight lanes of a group.
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (int o = 4; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
 
@@ -211,7 +220,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
 
@@ -274,8 +283,9 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
         ss = warp_sum(lane < (nt >> 5) ? red[0][lane] : 0.0f);
     }
     const float mean = __fdiv_rn(ss, (float)k) + eps;
-    // (a row of zeros without eps: zeros, not 0 * inf)
-    const float f = mean == 0.0f ? 0.0f : rsqrtf(mean);
+    // (a row of zeros without eps: zeros, not 0 * inf; a sum that overflowed, or
+    // a NaN in the row: NaN, not zeros)
+    const float f = mean == 0.0f ? 0.0f : mean < INFINITY ? rsqrtf(mean) : __uint_as_float(0x7FFFFFFFu);
     auto normed = [&](int i, float(&y)[16]) {
         const int u = tid + i * nt;
         const Unit g = u < units ? ld_unit(gain + 16 * u) : zero_unit();
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
         for (int i = 0; i < KEEP; i++) {
             float y[16];
             normed(i, y);
-            mx = fmaxf(mx, amax_16(y));
+            mx = max_nan(mx, amax_16(y));
         }
         mx = warp_max(mx);
         if (!WARP_ROW) {
