@@ -45,8 +45,10 @@
  *    workspace, which must not overlap either.
  *
  * Rounding: every quantised code and scale is defined bit-exactly (see each
- * function); GEMM and GEMV outputs are FP32 sums rounded once to BF16 and
- * agree with the exact sum within 1e-2*|out| + 1e-3*sum|a*w|.
+ * function), except that rmsnorm_residual_quant_fp8 and
+ * silu_mul_quant_fp8_per128 quantise an FP32 value y that carries a stated
+ * error; GEMM and GEMV outputs are FP32 sums rounded once to BF16 and agree
+ * with the exact sum within 1e-2*|out| + 1e-3*sum|a*w|.
  */
 #ifndef BSQ_H
 #define BSQ_H
@@ -396,7 +398,8 @@ BSQ_API bsq_status fp8_gemm_rowscale(const uint8_t *a, const float *a_scale,
  *                fp8_gemm_rowscale
  *   h = BF16_rne(x + residual) (FP32 sum; h = x without residual);
  *   y = (h * r) * gain, r = 1 / sqrt(sum h^2 / k + eps), all in FP32 and not
- *   rounded further; s = amax|y| / 448 over each group; q =
+ *   rounded further (within 2^-19 of itself; the order of the sum follows from
+ *   k alone, so a row's codes and scales do not depend on m); s = amax|y| / 448 over each group; q =
  *   E4M3_rne_satfinite(y / s); an all-zero group gives s = 0 and q = 0.
  *   sum h^2 must stay finite in FP32: a row where it does not, or that holds a
  *   NaN, gets NaN in all its codes and scales (a NaN gain in its groups').  A
@@ -427,7 +430,8 @@ BSQ_API bsq_status quant_act_fp8_per128(const uint16_t *a, uint8_t *a_fp8, float
  * silu_mul_quant_fp8_per128 -- the activation of a gated MLP, quantised for
  * the down projection: gate_up BF16 [m, 2k] (the gate's k columns, then the
  * up projection's k) -> E4M3 [m, k] + FP32 [m, k/128].
- *   y = (g / (1 + exp(-g))) * u in FP32, not rounded further, then the codes
+ *   y = (g / (1 + exp(-g))) * u in FP32, not rounded further (within 2^-20 of
+ *   itself while exp(-|g|) is a normal FP32 number, |g| <= 87), then the codes
  *   and scales of quant_act_fp8_per128 on y.  |y| must stay finite; a NaN
  *   gives NaN in its group's codes and scale.
  * Errors: k % 128 != 0 -> INVALID_ARG.  gate_up, a_fp8 16-byte aligned.

@@ -213,9 +213,23 @@ __global__ void __launch_bounds__(kThreads) k_silu_mul_quant_fp8_per128(const ui
 // RMS norm.  A row is held in registers as BF16 between the sum of squares and
 // the codes, KEEP units per thread: one warp per row (eight rows per CTA, no
 // barrier) up to K = 1024, else one CTA per row.
+//
+// The squares are added in an order that follows from K alone (a unit's
+// sixteen in turn, 32 units by halves, then those sums by halves), however
+// many units a thread holds, so a row alone and in a batch gives the same
+// bits.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+// Two sums over the warp, added as warp_sum does: a's in lanes 0 to 15, b's in
+// lanes 16 to 31.
+__device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
+    float v = lane & 16 ? b : a;
+    v += __shfl_xor_sync(0xFFFFFFFFu, lane & 16 ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
@@ -232,7 +246,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
                                              const uint16_t *__restrict__ gain, float eps, uint16_t *residual_out,
                                              uint8_t *__restrict__ q, float *__restrict__ scale, int per_row, int m,
                                              int k) {
-    __shared__ float red[2][32];
+    __shared__ float sums[WARP_ROW ? 1 : 32 * KEEP], maxima[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * kRowsPerCta + warp : blockIdx.x;
     const int tid = WARP_ROW ? lane : threadIdx.x, nt = WARP_ROW ? 32 : blockDim.x;
@@ -261,7 +275,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
                 h[i].w[j] = pack_bf16x2(__fadd_rn(lo_bf16(h[i].w[j]), lo_bf16(r[i].w[j])),
                                         __fadd_rn(hi_bf16(h[i].w[j]), hi_bf16(r[i].w[j])));
     }
-    float ss = 0.0f;
+    float sq[KEEP];
 #pragma unroll
     for (int i = 0; i < KEEP; i++) {
         const int u = tid + i * nt;
@@ -272,16 +286,32 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
         }
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            ss = fmaf(lo_bf16(h[i].w[j]), lo_bf16(h[i].w[j]), ss);
-            ss = fmaf(hi_bf16(h[i].w[j]), hi_bf16(h[i].w[j]), ss);
+            sq[i] = fmaf(lo_bf16(h[i].w[j]), lo_bf16(h[i].w[j]), j == 0 ? 0.0f : sq[i]);
+            sq[i] = fmaf(hi_bf16(h[i].w[j]), hi_bf16(h[i].w[j]), sq[i]);
         }
     }
-    ss = warp_sum(ss);
-    if (!WARP_ROW) {
-        if (lane == 0) red[0][warp] = ss;
+    float ss = 0.0f;
+    if (WARP_ROW) {
+#pragma unroll
+        for (int i = 0; i < KEEP; i++) ss += sq[i];
+    } else {
+        // units 32 c .. 32 c + 31 to sums[c]: warp + i * warps is the c of a warp's i-th units
+        const int warps = nt >> 5, all = KEEP * warps;
+        if (KEEP == 1) {
+            const float v = warp_sum(sq[0]);
+            if (lane == 0) sums[warp] = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < KEEP; i += 2) {
+                const float v = warp_sum2(sq[i], sq[i + (KEEP > 1)], lane);
+                if ((lane & 15) == 0) sums[warp + (i + (lane >> 4)) * warps] = v;
+            }
+        }
         __syncthreads();
-        ss = warp_sum(lane < (nt >> 5) ? red[0][lane] : 0.0f);
+#pragma unroll
+        for (int i = 0; i < KEEP; i++) ss += lane + 32 * i < all ? sums[lane + 32 * i] : 0.0f;
     }
+    ss = warp_sum(ss);
     const float mean = __fdiv_rn(ss, (float)k) + eps;
     // (a row of zeros without eps: zeros, not 0 * inf; a sum that overflowed, or
     // a NaN in the row: NaN, not zeros)
@@ -306,9 +336,9 @@ __global__ void __launch_bounds__(WARP_ROW ? 32 * kRowsPerCta : 1024)
         }
         mx = warp_max(mx);
         if (!WARP_ROW) {
-            if (lane == 0) red[1][warp] = mx;
+            if (lane == 0) maxima[warp] = mx;
             __syncthreads();
-            mx = warp_max(lane < (nt >> 5) ? red[1][lane] : 0.0f);
+            mx = warp_max(lane < (nt >> 5) ? maxima[lane] : 0.0f);
         }
         s = __fdiv_rn(mx, 448.0f);
         if (tid == 0) scale[row] = s;
