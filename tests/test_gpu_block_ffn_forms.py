@@ -1,0 +1,97 @@
+"""GPU tests of the block-FP8 feed-forward operators by form: every size is
+chosen by the rule that selects a kernel's form, and compared with the 64-bit
+definition."""
+import pytest
+import torch
+
+import int8_gemm_gemv_b200 as bsq
+from test_gpu_block_ffn import DEV, F8, check_gemm, codes, dequant_a, dequant_w, gen, poisoned, run_gemm, scales
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _no_timeouts():
+    yield
+    assert bsq.debug_take_timeouts() == 0
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def many_rows(m, n):
+    """Whether the product runs on CTA pairs: more than 64 rows, and more tiles of 128 x 32 than SMs."""
+    return m > 64 and -(-n // 128) * -(-m // 32) > sms()
+
+
+# --------------------------------------------------- product, CTA pairs ---
+
+@pytest.mark.parametrize("k", [128, 256, 384, 640, 1408, 5120, 17408])
+def test_pair_depths(k):
+    assert many_rows(1100, 640)
+    run_gemm(1100, 640, k, seed=k)
+
+
+@pytest.mark.parametrize("m,n", [(1300, 577), (1300, 584), (1300, 639), (1300, 641), (1300, 648), (1300, 1001),
+                                 (5000, 1), (5000, 7), (5000, 8), (5000, 64), (5000, 100), (5000, 130)])
+def test_pair_columns(m, n):
+    """Rows stored by TMA, and rows of an odd length stored one by one; tiles that end inside a scale block."""
+    assert many_rows(m, n)
+    run_gemm(m, n, 384, seed=n)
+
+
+@pytest.mark.parametrize("m", [1153, 1279, 1281, 1407, 1535, 1537, 4737])
+def test_pair_rows(m):
+    """The last tile with 1 to 256 rows; several tiles to a CTA pair."""
+    n = 2112 if m > 4096 else 520
+    assert many_rows(m, n)
+    run_gemm(m, n, 512, seed=m)
+
+
+def test_pair_exact_sums():
+    """Small integers and power-of-two scales: the correctly rounded value, whatever the order."""
+    m, n, k = 1100, 640, 1024
+    assert many_rows(m, n)
+    g = gen(11)
+    a = torch.randint(-4, 5, (m, k), device=DEV, generator=g).float().to(F8).view(torch.uint8)
+    w = torch.randint(-4, 5, (n, k), device=DEV, generator=g).float().to(F8).view(torch.uint8)
+    sa = 2.0 ** torch.randint(-2, 3, (m, k // 128), device=DEV, generator=g).float()
+    sw = 2.0 ** torch.randint(-2, 3, (n // 128, k // 128), device=DEV, generator=g).float()
+    out = poisoned((m, n), torch.bfloat16)
+    bsq.fp8_gemm_blockscaled(a, sa, w, sw, out, m, n, k)
+    assert torch.equal(out, (dequant_a(a, sa) @ dequant_w(w, sw).t()).float().bfloat16())
+
+
+@pytest.mark.parametrize("blocks", [4, 5])
+def test_pair_scales_are_per_block(blocks):
+    """One K block and one N block at a time carry a non-zero scale (K blocks in fours, and one more)."""
+    m, n, k = 1100, 640, 128 * blocks
+    assert many_rows(m, n)
+    a, w = codes((m, k), 20), codes((n, k), 21)
+    for kb in range(blocks):
+        for nb in range(n // 128):
+            sa, sw = torch.zeros(m, blocks, device=DEV), torch.zeros(n // 128, blocks, device=DEV)
+            sa[:, kb] = 1 + torch.arange(m, device=DEV) / 64
+            sw[nb, kb] = 0.5
+            out = poisoned((m, n), torch.bfloat16)
+            bsq.fp8_gemm_blockscaled(a, sa, w, sw, out, m, n, k)
+            check_gemm(out, a, sa, w, sw, (kb, nb))
+            other = torch.ones(n, dtype=torch.bool, device=DEV)
+            other[128 * nb:128 * nb + 128] = False
+            assert (out[:, other] == 0).all()
+
+
+@pytest.mark.parametrize("m,n", [(1, 640), (16, 640), (40, 640), (1100, 640), (1300, 577)])
+@pytest.mark.parametrize("k", [512, 640, 2048])
+@pytest.mark.parametrize("off_a,off_w", [(1, 0), (0, 1), (3, 2)])
+def test_product_with_scales_on_4_byte_addresses(m, n, k, off_a, off_w):
+    """Scale matrices that start one to three floats past a 16-byte boundary."""
+    a, w = codes((m, k), 1), codes((n, k), 2)
+    sa = scales((m * (k // 128) + off_a,), 3)[off_a:].view(m, k // 128)
+    sw = scales((-(-n // 128) * (k // 128) + off_w,), 4)[off_w:].view(-1, k // 128)
+    assert sa.data_ptr() % 16 == 4 * off_a and sw.data_ptr() % 16 == 4 * off_w
+    out = poisoned((m + 1, n), torch.bfloat16)
+    bsq.fp8_gemm_blockscaled(a, sa, w, sw, out, m, n, k)
+    check_gemm(out[:m], a, sa, w, sw, (m, n, k))
+    assert out[m].isnan().all()
