@@ -1,11 +1,14 @@
 """GPU tests of the block-FP8 feed-forward operators by form: every size is
 chosen by the rule that selects a kernel's form, and compared with the 64-bit
-definition."""
+definition (or, where codes are exact, with the oracle)."""
+import numpy as np
 import pytest
 import torch
 
 import int8_gemm_gemv_b200 as bsq
-from test_gpu_block_ffn import DEV, F8, check_gemm, codes, dequant_a, dequant_w, gen, poisoned, run_gemm, scales
+import oracle
+from test_gpu_block_ffn import (DEV, F8, U32, activations, check_codes, check_gemm, codes, dequant_a, dequant_w, gen,
+                                norm_exact, norm_rel, poisoned, run_gemm, scales)
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +98,54 @@ def test_product_with_scales_on_4_byte_addresses(m, n, k, off_a, off_w):
     bsq.fp8_gemm_blockscaled(a, sa, w, sw, out, m, n, k)
     check_gemm(out[:m], a, sa, w, sw, (m, n, k))
     assert out[m].isnan().all()
+
+
+# ------------------------------------------- producers, two units a lane ---
+
+def two_units(m, k):
+    return m * k // 16 >= sms() * 2048 * 3
+
+
+# the last CTA holds 512 units where all are in range; these leave it a part of its first or second 256
+@pytest.mark.parametrize("m,k", [(23000, 640), (7700, 1920), (1003, 17408), (120001, 128)])
+def test_quantiser_two_units(m, k):
+    assert two_units(m, k) and m * k // 16 % 512
+    x = activations(m, k, 1)
+    q, s = poisoned((m + 1, k), torch.uint8), poisoned((m + 1, k // 128), torch.float32)
+    bsq.quant_act_fp8_per128(x, q, s, m, k)
+    assert (q[m] == 0xFF).all() and s[m].isnan().all()
+    for rows in (slice(0, 150), slice(m // 2, m // 2 + 150), slice(m - 150, m)):
+        oq, os_ = oracle.quant_rowwise_fp8(x[rows].view(torch.int16).cpu().numpy().view(np.uint16).reshape(-1, 128))
+        assert np.array_equal(q[rows].cpu().numpy().reshape(-1, 128), oq)
+        assert np.array_equal(s[rows].cpu().numpy().reshape(-1), os_)
+    check_codes(q[:m], s[:m], x.double(), 128, 0.0, (m, k))
+
+
+@pytest.mark.parametrize("m,k", [(23000, 640), (7700, 1920), (1003, 17408), (120001, 128)])
+def test_silu_two_units(m, k):
+    assert two_units(m, k) and m * k // 16 % 512
+    x = activations(m, 2 * k, 2)
+    q, s = poisoned((m + 1, k), torch.uint8), poisoned((m + 1, k // 128), torch.float32)
+    bsq.silu_mul_quant_fp8_per128(x, q, s, m, k)
+    g, u = x.double().split(k, dim=1)
+    check_codes(q[:m], s[:m], g * torch.sigmoid(g) * u, 128, 6 * U32, (m, k))
+    assert (q[m] == 0xFF).all() and s[m].isnan().all()
+
+
+@pytest.mark.parametrize("group", [128, 0])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("m,k", [(600, 5120), (2100, 2688), (700, 4224), (200, 16384), (5, 20480), (4, 40960), (3, 65536)])
+def test_norm_two_and_four_units(m, k, residual, group):
+    """A CTA per row with two units per thread (the long prefill's form) and, beyond K = 32768, four."""
+    assert (k // 16 > 160 and m * (k // 16) > 1024 * sms()) or k // 16 > 1024
+    x, r = activations(m, k, 3), activations(m, k, 4)
+    gain = (1 + 0.2 * torch.randn(k, device=DEV, generator=gen(5))).bfloat16()
+    h = (x.float() + r.float()).bfloat16() if residual else x
+    out = poisoned((m, k), torch.bfloat16) if residual else None
+    q = poisoned((m + 1, k), torch.uint8)
+    s = poisoned((m + 1, k // group) if group else (m + 1,), torch.float32)
+    bsq.rmsnorm_residual_quant_fp8(x, r if residual else None, gain, 1e-6, out, q, s, group, m, k)
+    if residual:
+        assert torch.equal(out.view(torch.int16), h.view(torch.int16))
+    check_codes(q[:m], s[:m], norm_exact(h, gain, 1e-6), group, norm_rel(k), (m, k, residual, group))
+    assert (q[m] == 0xFF).all() and s[m].isnan().all()
