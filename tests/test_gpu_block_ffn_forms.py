@@ -7,7 +7,7 @@ import torch
 
 import int8_gemm_gemv_b200 as bsq
 import oracle
-from test_gpu_block_ffn import (DEV, F8, U32, activations, check_codes, check_gemm, codes, dequant_a, dequant_w, gen,
+from test_gpu_block_ffn import (DEV, F8, Moe, U32, activations, check_codes, check_gemm, codes, dequant_a, dequant_w, gen,
                                 norm_exact, norm_rel, poisoned, run_gemm, scales)
 
 pytestmark = pytest.mark.gpu
@@ -149,3 +149,37 @@ def test_norm_two_and_four_units(m, k, residual, group):
         assert torch.equal(out.view(torch.int16), h.view(torch.int16))
     check_codes(q[:m], s[:m], norm_exact(h, gain, 1e-6), group, norm_rel(k), (m, k, residual, group))
     assert (q[m] == 0xFF).all() and s[m].isnan().all()
+
+
+# ------------------------------------------ expert layer, choice by rounds ---
+
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("e,topk", [(64, 8), (300, 8), (512, 16)])
+def test_moe_routing_corners_by_rounds(e, topk, renorm):
+    """The corners of the choice of experts where it is made by rounds of a maximum: beyond 2^15 tokens x experts^2."""
+    t = 16
+    assert t * e * e > 1 << 15
+    l = torch.randn(t, e, device=DEV, generator=gen(1))
+    l[0] = -torch.inf  # nothing may be chosen
+    l[1] = 0.0  # all tie: the lowest indices
+    l[2, 5:] = -torch.inf  # fewer candidates than choices
+    l[3, 7] = torch.nan  # counts as -inf
+    l[3, 9] = torch.inf  # certain
+    l[4] = -0.0
+    l[4, 30] = 0.0  # equals -0
+    l[5, 3] = 90.0  # others' weights underflow
+    l[6] = torch.finfo(torch.float32).min  # masks of the type's lowest value
+    l[6, 11] = 1.0
+    l[7] = torch.nan
+    l[8] = torch.inf  # all certain
+    l[9] = l[9].round()  # many ties
+    l[10] = -l[10].abs().round()
+    l[11, ::32] = 7.0  # ties among one lane's experts
+    l[12, 1::2] = -torch.inf
+    l[13, e - 3:] = 50.0  # the last experts
+    l[14, 32:] = torch.nan
+    l[15] = torch.arange(e, device=DEV) * 1e-3
+    m = Moe(t, 256, 128, e, topk, renorm, seed=5, logits=l)
+    m()
+    m.check((e, renorm))
+    assert (m.out[0] == 0).all() and (m.out[7] == 0).all()
