@@ -303,6 +303,8 @@ bsq_status check_moe_shape(int tokens, int hidden, int inter, int topk) {
 
 size_t fp8_moe_workspace_bytes(int tokens, int hidden, int inter, int topk) {
     if (check_moe_shape(tokens, hidden, inter, topk) != BSQ_OK) return 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;  // the size depends on the device's SMs
     return bsq::fp8_moe_workspace_bytes(tokens, hidden, inter, topk);
 }
 
