@@ -23,9 +23,6 @@ namespace {
 
 using namespace qc;
 
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 struct Unit {
     uint32_t w[8];  // sixteen BF16 values, element 2j in the low half of w[j]
 };

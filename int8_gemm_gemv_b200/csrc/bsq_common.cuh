@@ -31,6 +31,18 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // never hang the GPU.  Legitimate waits last microseconds.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
+// Programmatic stream serialization: the wait for the kernels before this one,
+// and the leave for the next to start (it waits in its turn).
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// (d0, d1) += (a0, a1) * (b0, b1), packed
+__device__ __forceinline__ void fma2(float2 &d, float2 a, float2 b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+}
+
 // One lane of a converged warp, chosen by elect.sync.  Inside a branch on it
 // the compiler knows that a single thread runs, and issues tensor-core and
 // copy instructions at their full rate; under `lane == 0` it does not (a
@@ -87,6 +99,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, unsign
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             atomicOr(timeout_flag, 1u);
             return false;
+        }
+    }
+}
+
+// The same for warps that reach the end of their loops and barriers together,
+// without a vote in the loop: a wait that runs out sets the CTA's abort flag
+// and goes on, and once that is set every wait returns at once.
+__device__ __forceinline__ void mbar_wait_or_abort(uint64_t *bar, uint32_t parity, volatile uint32_t *abort,
+                                                   unsigned int *timeout_flag) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(timeout_flag, 1u);
+            *abort = 1;
+            return;
         }
     }
 }

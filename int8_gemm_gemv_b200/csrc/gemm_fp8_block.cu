@@ -50,16 +50,6 @@ namespace {
 
 static __device__ unsigned int g_timeouts;
 
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// (d0, d1) += (a0, a1) * (b0, b1), packed
-__device__ __forceinline__ void fma2(float2 &d, float2 a, float2 b) {
-    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(*reinterpret_cast<uint64_t *>(&d))
-        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
-}
-
 // Pair MMA: D (128 lanes of each CTA) (+)= A (128 rows in each CTA) x
 // B (N rows, half in each CTA), E4M3, issued by the even CTA.  The low words
 // of the descriptors (start address) vary; the high word is the same for all.
@@ -109,19 +99,8 @@ static_assert(kSmemBytes <= 232448, "shared memory per block");
 
 __device__ __forceinline__ bool aborted(volatile Smem *s) { return s->abort != 0; }
 
-// Bounded wait that sets the abort flag when it runs out, and returns without
-// waiting once that flag is set.
 __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, Smem *S) {
-    if (mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (aborted(S)) return;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(&g_timeouts, 1u);
-            *(volatile uint32_t *)&S->abort = 1;
-            return;
-        }
-    }
+    mbar_wait_or_abort(bar, parity, &S->abort, &g_timeouts);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -324,9 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll 1
                 for (int j = 0; j < min(SG, nkb - kb0); j += GB) {
-                    // A wait that runs out sets the abort flag and goes on:
-                    // every later wait then returns at once, and all warps
-                    // reach the end without a vote in the loop.
                     if (!ready) wait_or_abort(&S->tfull[b], bph, S);
                     __syncwarp();
                     tc_fence_after();

@@ -64,19 +64,8 @@ template <int NT> size_t smem_bytes(int stages) {
 
 template <int NT> __device__ __forceinline__ bool aborted(volatile Smem<NT> *s) { return s->abort != 0; }
 
-// Bounded wait that sets the abort flag when it runs out, and returns without
-// waiting once that flag is set.
 template <int NT> __device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, Smem<NT> *S) {
-    if (mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (aborted<NT>(S)) return;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(&g_timeouts, 1u);
-            *(volatile uint32_t *)&S->abort = 1;
-            return;
-        }
-    }
+    mbar_wait_or_abort(bar, parity, &S->abort, &g_timeouts);
 }
 
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -88,11 +77,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld_32x32b_x8(taddr, r); }
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 
-__device__ __forceinline__ void fma2(float2 &d, float2 a, float2 b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;"
-        : "+l"(*reinterpret_cast<uint64_t *>(&d))
-        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
-}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -147,10 +131,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // only now: a dependent must not take the tensor memory first
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    launch_dependents();  // only now: a dependent must not take the tensor memory first
     const uint32_t tmem = S->tmem_base;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    dependency_wait();
 
     if (warp == 0) {
         if (elect_one()) {
@@ -254,8 +237,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         int b = 0, ss = 0;
         uint32_t bph = 0, sph = 0;
         for (int it = 0; it < nkb; it++) {
-            // a wait that runs out sets the abort flag and goes on, so all
-            // warps reach the end (and the cluster barriers) together
             if (it % SG == 0) wait_or_abort<NT>(&S->sfull[ss], sph, S);
             wait_or_abort<NT>(&S->tfull[b], bph, S);
             __syncwarp();

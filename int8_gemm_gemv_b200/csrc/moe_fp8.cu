@@ -22,8 +22,8 @@
 //                  and one of up rows give silu(g) * u on the spot.  act is
 //                  kept as FP16 times a power of two per 16 values, 11
 //                  significant bits: the down product's MMAs are FP16, and a
-//                  second FP16 for the rest would double them for less than a
-//                  tenth of the output's own BF16 rounding.
+//                  second FP16 for the rest would double them for about a tenth
+//                  of the output's own BF16 rounding.
 //   k_moe_down     an output tile of 64 or 128 rows runs over all reached experts'
 //                  K, so a token's experts add up in registers.  act enters
 //                  the MMAs at one power of two per token and scale block,
@@ -116,7 +116,6 @@ __device__ __forceinline__ void ld_32b_if(bool p, const void *src, uint32_t (&v)
         : "l"(src), "r"((int)p)
         : "memory");
 }
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- routing --
 
@@ -258,22 +257,6 @@ static_assert(kMoeMaxExperts % (32 * kConsumers) == 0 && kMoeMaxExperts / 32 <= 
 
 // ------------------------------------------------------------------- ring --
 
-// Bounded wait that sets the abort flag when it runs out, and returns without
-// waiting once that flag is set: the warps then reach the end of their loops
-// and barriers together, without a vote in the loop.
-__device__ __forceinline__ void wait_or_abort(uint64_t *bar, uint32_t parity, Bars *S) {
-    if (mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*(volatile uint32_t *)&S->abort) return;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(&g_timeouts, 1u);
-            *(volatile uint32_t *)&S->abort = 1;
-            return;
-        }
-    }
-}
-
 // Consumer side of the ring: every consumer warp takes its part of every slot.
 struct Taker {
     int s = 0;
@@ -283,7 +266,7 @@ struct Taker {
     __device__ __forceinline__ Taker(Bars *S) : empty0(mapa_shared(smem_u32(&S->empty[0]), 0)) {}
     // Waits for the next slot; returns its address in shared memory.
     __device__ __forceinline__ uint32_t take(Bars *S, uint32_t ring, int slot_bytes) {
-        wait_or_abort(&S->full[s], ph, S);
+        mbar_wait_or_abort(&S->full[s], ph, &S->abort, &g_timeouts);
         __syncwarp();
         return ring + (uint32_t)s * slot_bytes;
     }
@@ -463,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dependency_wait();
     // the down kernel may start where CTAs run out; it reads nothing that this
     // one writes before it has completed, and everything before this one has
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    launch_dependents();
 
     route(a, R, reinterpret_cast<uint32_t *>(red));
 
@@ -684,13 +667,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) give.give_up(S, ring.slots);
             dependency_wait();  // no CTA ends before the previous kernel has
-            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            launch_dependents();
         }
         return;
     }
 
     dependency_wait();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    launch_dependents();
     if (all == 0) {  // no token has an expert
         for (int64_t i = (int64_t)blockIdx.x * 32 * kConsumers + threadIdx.x; i < (int64_t)T * H;
              i += (int64_t)gridDim.x * 32 * kConsumers)
