@@ -407,11 +407,15 @@ cudaError_t launch_rmsnorm_residual_quant_fp8(const uint16_t *x, const uint16_t 
     };
     if (units <= 32) return warp_rows(k_rmsnorm_residual_quant_fp8<1, true>);
     if (units <= 64) return warp_rows(k_rmsnorm_residual_quant_fp8<2, true>);
-    // One unit per thread for short rows (8192 x 1040: 16.6 us, 19.0 with two),
-    // for no more rows than SMs (1 x 5120: 2.6 us, 3.4 with two), and where all
-    // rows of a medium length are resident at once (300 x 5120: 4.6 us, 5.4
-    // with two); else two, which keep more loads in flight per warp (8192 x
-    // 5120: 48.6 us, 51.7 with one; 1000 x 16384: 24.0 us, 30.0 with one).
+    // One unit per thread for short rows (4000 rows: 160 units 15.3 us, 15.8
+    // with two; 168 units 16.8 and 16.4), for no more rows than SMs (1024 units:
+    // 148 rows 5.0 and 5.1, 160 rows 8.1 and 7.0), and, for a medium length,
+    // while the rows have no more than 1024 units per SM (320 units: 470 rows
+    // 5.3 and 6.7, 600 rows 6.2 and 6.8, 1000 rows 9.5 and 9.4, 4000 rows 28.7
+    // and 26.2); else two, which keep more loads in flight per warp (4000 x
+    // 1024 units: 78.0 us, 109.1 with one).  The lengths that count as medium
+    // end where such batches stop gaining (470 rows: 384 units 6.0 and 6.9, 392
+    // units 6.6 and 6.4, 512 units 7.7 and 7.1).  Scale per row.
     const int64_t sms = sm_count();
     if (units <= 160 || (units <= 384 && (int64_t)m * units <= 1024 * sms) || (units <= 1024 && m <= sms))
         return cta_rows(k_rmsnorm_residual_quant_fp8<1, false>, 1);

@@ -449,11 +449,15 @@ uint32_t take_timeouts_gemm_fp8_block() {
     return v;
 }
 
-// The swapped-operand kernel up to 64 rows (64 x 17408 x 5120: 19.4 us against
-// 23.9 here; 64 x 5120 x 5120: 11.6 against 13.3), and beyond while its tiles
-// of 128 x 32 outputs fit one to an SM (128 x 2112 x 5120, 68 tiles: 9.7 us
-// against 12.5; 256 x 2112 x 5120, 136 tiles: 12.7 both; 128 x 5120 x 5120,
-// 160 tiles: 17.5 against 13.6).
+// The swapped-operand kernel up to 64 rows (64 x 17408 x 5120: 19.6 us against
+// 23.7 here, 65 rows 32.1 against 24.0; 64 x 5120 x 5120: 11.5 against 13.1),
+// and beyond while its tiles of 128 x 32 outputs fit one to an SM (x 5120 x
+// 5120: 96 rows, 120 tiles, 12.9 against 13.4; 128 rows, 160 tiles, 17.3
+// against 13.5; x 2112 x 5120: 128 rows, 68 tiles, 10.5 against 12.7; 256 rows,
+// 136 tiles, 12.7 both; 320 rows, 170 tiles, 17.6 against 12.8).  K moves this
+// bound little (x 5120 x 17408: 96 rows 36.0 against 34.9, 128 rows 51.1
+// against 35.0; x 5120 x 1408: 96 rows 5.7 against 7.0, 128 rows 7.0 against
+// 7.2).  Back to back in a graph, weights rotated past L2.
 cudaError_t launch_fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w,
                                         const float *w_scale, uint16_t *out, int m, int n, int k, cudaStream_t s) {
     const int64_t small_tiles = (int64_t)((n + 127) / 128) * ((m + 31) / 32);
