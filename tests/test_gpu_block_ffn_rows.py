@@ -51,3 +51,30 @@ def test_quantisers_of_a_row_do_not_depend_on_the_batch(k):
         for m in (bound + 1, bound + 7, bound + 33, bound - 1, 5):
             part = rows_of(call, y, m, k, k // 128)
             assert torch.equal(part[0], whole[0][:m]) and torch.equal(part[1], whole[1][:m]), (width, m)
+
+
+@pytest.mark.parametrize("k", [128, 1024, 1152, 5120, 16384, 65536])
+def test_error_of_the_quantised_values(k):
+    """The scale is amax|y| / 448 rounded once, so it shows the error of y:
+    within 2^-19 of itself for the norm, 2^-20 for SiLU (|g| <= 87).
+
+    Norm: a square and its addition 16 times in a unit, five additions over 32
+    units, at most 4 + 5 over those sums, half of it after the root: 15 x 2^-24;
+    division and eps half a rounding each, rsqrt 2 ulp, two products: 22 x 2^-24.
+    SiLU: exp 2 ulp, 1 + z half an ulp, the reciprocal one, three products half
+    each: 5 x 2^-23.  (A gate below -87, where exp loses bits, gives a y near
+    2^-120 here, never a group's largest; above 87 1 + z is 1 either way.)"""
+    m = 64
+    x, gain = activations(m, k, 5), activations(1, k, 6)[0]
+    for group in (0, 128):
+        q, s = poisoned((m, k), torch.uint8), poisoned((m, k // group if group else 1), torch.float32)
+        bsq.rmsnorm_residual_quant_fp8(x, None, gain, 1e-6, None, q, s, group, m, k)
+        y = x.double() / torch.sqrt((x.double()**2).mean(1, keepdim=True) + 1e-6) * gain.double()
+        want = y.abs().view(m, -1, group or k).amax(-1) / 448
+        assert ((s.double() - want).abs() <= (2.0**-19 + 2.0**-23) * want).all(), (k, group)
+    x = activations(m, 2 * k, 7)
+    q, s = poisoned((m, k), torch.uint8), poisoned((m, k // 128), torch.float32)
+    bsq.silu_mul_quant_fp8_per128(x, q, s, m, k)
+    g, u = x.double().split(k, dim=1)
+    want = (g * torch.sigmoid(g) * u).abs().view(m, -1, 128).amax(-1) / 448
+    assert ((s.double() - want).abs() <= (2.0**-20 + 2.0**-23) * want).all(), k
