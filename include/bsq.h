@@ -399,8 +399,9 @@ BSQ_API bsq_status fp8_gemm_rowscale(const uint8_t *a, const float *a_scale,
  *   h = BF16_rne(x + residual) (FP32 sum; h = x without residual);
  *   y = (h * r) * gain, r = 1 / sqrt(sum h^2 / k + eps), all in FP32 and not
  *   rounded further (within 2^-19 of itself; the order of the sum follows from
- *   k alone, so a row's codes and scales do not depend on m); s = amax|y| / 448 over each group; q =
- *   E4M3_rne_satfinite(y / s); an all-zero group gives s = 0 and q = 0.
+ *   k alone, so a row's codes and scales do not depend on m);
+ *   s = amax|y| / 448 over each group; q = E4M3_rne_satfinite(y / s); an
+ *   all-zero group gives s = 0 and q = 0.
  *   sum h^2 must stay finite in FP32: a row where it does not, or that holds a
  *   NaN, gets NaN in all its codes and scales (a NaN gain in its groups').  A
  *   square below FP32's normal range loses bits or counts as 0, and a row
@@ -434,6 +435,8 @@ BSQ_API bsq_status quant_act_fp8_per128(const uint16_t *a, uint8_t *a_fp8, float
  *   itself while exp(-|g|) is a normal FP32 number, |g| <= 87), then the codes
  *   and scales of quant_act_fp8_per128 on y.  |y| must stay finite; a NaN
  *   gives NaN in its group's codes and scale.
+ * There is no form with one scale per row: in front of fp8_gemm_rowscale, form
+ * y in BF16 and use quant_rowwise_fp8.
  * Errors: k % 128 != 0 -> INVALID_ARG.  gate_up, a_fp8 16-byte aligned.
  * ---------------------------------------------------------------------- */
 BSQ_API bsq_status silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *a_fp8,
@@ -446,7 +449,11 @@ BSQ_API bsq_status silu_mul_quant_fp8_per128(const uint16_t *gate_up, uint8_t *a
  *   a E4M3 [m, k] + a_scale FP32 [m, k/128]; w E4M3 [n, k] + w_scale FP32
  *   [ceil(n/128), k/128] (n need not be a multiple of 128); out BF16 [m, n].
  *   C[i,j] = sum_b a_scale[i,b] * w_scale[j/128,b] * sum_{k in b} a*w
- * FP32 sums, one BF16 rounding.  a, w, out 16-byte aligned, scales 4-byte.
+ * FP32 sums, one BF16 rounding.  The two scales of a block are multiplied
+ * first, in FP32: their product must be finite, and one below FP32's normal
+ * range loses bits or counts as 0.  The order of the sum depends on m (the
+ * number of rows selects the kernel and how K is split).  a, w, out 16-byte
+ * aligned, scales 4-byte.
  * Errors: k % 16 != 0 -> INVALID_ARG; k % 128 != 0 -> UNSUPPORTED.
  * ---------------------------------------------------------------------- */
 BSQ_API bsq_status fp8_gemm_blockscaled(const uint8_t *a, const float *a_scale, const uint8_t *w,
