@@ -64,8 +64,7 @@ __device__ __forceinline__ uint32_t e4m3x4(uint64_t a, uint64_t b) {
 // either side of RN(y / s) (their own roundings are 2^-24 each): where the
 // codes of both agree they are the answer, for all sixteen in one comparison.
 // Otherwise the pairs that differ are settled one by one.  (A branch per pair,
-// at 2^-16, instead: SiLU 2048 x 17408 37.8 us, 34.7 so; norm 8192 x 5120 48.1
-// and 46.5.)
+// at 2^-16, instead: SiLU 2048 x 17408 9% and norm 8192 x 5120 3% slower.)
 __device__ __forceinline__ uint4 codes_16(const float (&y)[16], float s) {
     if (s == 0.0f) return make_uint4(0u, 0u, 0u, 0u);
     const Bracket br = bracket_of(s);
@@ -369,9 +368,11 @@ cudaError_t launch_pss(void (*kernel)(P...), int64_t grid, int threads, cudaStre
     return e;
 }
 
-// Units per lane: two where that still gives the SMs three times the threads
-// they hold or more (quantiser 4096 x 17408: 39.6 us, 44.0 with one, 55.0 with
-// four), one below (512 x 17408: 6.8 us, 7.4 with two).
+// Units per lane: two where the units are three times the threads the SMs hold
+// or more (836 rows of 17408: quantiser 10.9 us, 11.3 with one, SiLU 15.7 and
+// 15.8; 4096 rows: 39.6 and 43.9, 63.4 and 67.3, the quantiser with four
+// 55.0), one below (512 rows: quantiser 7.9 us, 8.2 with two, SiLU 10.5 and
+// 10.7; 128 rows: 3.6 and 4.6, 4.5 and 5.9).
 bool two_units(int64_t units) { return units >= (int64_t)sm_count() * 2048 * 3; }
 int64_t grid_for_units(int64_t units, int unroll) { return (units + (int64_t)kThreads * unroll - 1) / (kThreads * unroll); }
 

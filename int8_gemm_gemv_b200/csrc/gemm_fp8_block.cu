@@ -26,14 +26,14 @@
 //               and TMA stores (plain stores where a row is not a multiple of
 //               16 bytes)
 // Per SM and K block the MMAs take 256 cycles and the fold's 16,384 FMAs 64 to
-// 128 of the FP32 lanes' cycles; a block takes about 420.  What is between is
+// 128 of the FP32 lanes' cycles; a block takes about 455.  What is between is
 // the round of a buffer: MMAs, commit, the waiting warps' wake-up, two
 // tensor-memory loads of 64 columns, the arrival at the even CTA.  Two blocks
 // per stage halve the rounds, and the issue takes about 50 cycles per MMA
 // (elected thread, precomputed descriptor words), under the 64 that it runs.
-// 4096 x 17408 x 5120: 340 to 400 us by operands' values (1.83 to 2.15
-// PFLOP/s; the power limit acts), 225 at twice the BF16 rate of a plain
-// product.  Tiles of 256 x 256 (fold of 128 registers per thread, 16 or 8
+// 4096 x 17408 x 5120: 344 to 358 us by operands' values in a burst (2.04 to
+// 2.12 PFLOP/s), 408 when repeated for seconds, where the power limit holds the
+// clock at 1.43 GHz; 225 at twice the BF16 rate of a plain product.  Tiles of 256 x 256 (fold of 128 registers per thread, 16 or 8
 // warps), one block per stage, and two tiles in turn were not faster.
 //
 // Launched with programmatic stream serialization: every role waits for the

@@ -8,7 +8,11 @@
 // (a cluster of 1 to 8) share a tile, each streaming its share of the K
 // blocks; their FP32 sums are added through distributed shared memory in rank
 // order, so the result does not depend on timing and no workspace is needed.
-// Small rings let two CTAs share an SM.
+// Small rings let two CTAs share an SM.  16 x 5120 x 5120: 8.9 us back to back in
+// a graph with the weight rotated past L2 (6.8 with it in L2), where a kernel
+// that only reads the weight takes 5.6 and the copy peak 4.0: what is above the
+// stream is the start of the ring behind the previous kernel and the join of a
+// tile's sums.
 //
 // Per CTA (384 threads):
 //   warp 0      TMA producer: one K block per stage (16 KB of W, NT x 128
